@@ -416,7 +416,8 @@ def _store8(pages, scales, x, b, pos, page, slot, start, new, s):
     at = page * per + slot // block
     most.scatter_reduce_(0, at[:, None].expand(-1, Hkv), size, "amax")
     m, e = torch.frexp(most)
-    need = torch.exp2((e - 8 - (m <= 0.875).int()).clamp(-64, 64).float())
+    e = torch.where(most > 0, e - 8 - (m <= 0.875).int(), -64)
+    need = torch.exp2(e.clamp(-64, 64).float())
     touched = torch.zeros(P * per, dtype=torch.bool, device="cuda")
     touched[at] = True
     # the block in which a sequence's new rows begin, where it has cached rows before them
