@@ -186,6 +186,21 @@ int device_error_word(unsigned int** err, int* num_sms) {
     *num_sms = s->num_sms;
     return FA_OK;
 }
+
+int call_workspace(void* workspace, int given, size_t need, cudaStream_t stream, void** out) {
+    if (workspace) {
+        if (given < 0 || static_cast<size_t>(given) < need) return FA_ERR_SHAPE;
+        *out = workspace;
+        return FA_OK;
+    }
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &capture) != cudaSuccess) return FA_ERR_CUDA;
+    if (capture != cudaStreamCaptureStatusNone) return FA_ERR_UNSUPPORTED;
+    DeviceState* s = nullptr;
+    int rc = lookup_device(&s);
+    if (rc != FA_OK) return rc;
+    return ensure_workspace(s, need, stream, out);
+}
 }  // namespace fa
 
 namespace {

@@ -120,6 +120,16 @@ int launch_decode_pack(const int32_t* block_table, int max_pages, const int32_t*
 // The current device's error word and SM count (sm_100 devices only).
 int device_error_word(unsigned int** err, int* num_sms);
 
+// A call's scratch: the caller's (`given` bytes, FA_ERR_SHAPE if they are fewer
+// than `need`), or with none given the library's workspace of the stream.  The
+// library's is refused (FA_ERR_UNSUPPORTED) while the stream is being captured:
+// an allocation would belong to the graph, and a second graph of the stream
+// would hold the same addresses.
+int call_workspace(void* workspace, int given, size_t need, cudaStream_t stream, void** out);
+
+// ---- rotary tables, norms with the rotation --------------------------------
+constexpr int kRopeMaxPairs = 128;  // of a table's row
+
 int launch_append(const void* k_new, const void* v_new, const int32_t* cu_new, void* k_pages,
                   void* v_pages, const int32_t* page_table, const int32_t* seq_lens, int B,
                   int Hk, int total_new, int d, int page_size, int num_pages, void* workspace,

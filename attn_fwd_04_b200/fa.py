@@ -30,6 +30,9 @@ EXPORTS = ("fa_fwd", "fa_fwd_gqa", "fa_fwd_rope", "fa_bwd", "fa_bwd_gqa", "fa_bw
            "fa_decode_paged_gqa", "fa_decode_paged_strided",
            "fa_decode_paged_noalloc", "fa_append_paged", "fa_prefill_paged",
            "fa_gather_paged",
+           "fa_rope_table", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+           "fa_qk_norm_rope_bwd_workspace", "fa_append_paged_rope", "fa_append_paged_fp8",
+           "fa_decode_paged_fp8", "fa_decode_paged_fp8_workspace",
            "fa_get_device_error", "fa_selftest_bounded_wait", "fa_selftest_fwd_stall",
            "fa_selftest_decode_stall",
            "fa_release_workspace", "fa_status_str", "fa_version", "fa_fwd_set_cta_pairs")
@@ -67,6 +70,19 @@ def lib() -> ctypes.CDLL:
         L.fa_gather_paged.argtypes = [P, P, P, P, I, I, I, I, P]
         L.fa_append_paged.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, P]
         L.fa_prefill_paged.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, F, P]
+        D = ctypes.c_double
+        L.fa_rope_table.argtypes = [P, P, I, I, D, I, D, I, D, D, D, P]
+        L.fa_qk_norm_rope.argtypes = [P] * 6 + [I, P, P, I, I, I, P] + [I] * 10 + [F, P]
+        L.fa_qk_norm_rope_bwd.argtypes = ([P] * 10 + [I, P, P, I, I, I, P] + [I] * 12 +
+                                          [F, P, I, P])
+        L.fa_qk_norm_rope_bwd_workspace.argtypes = [I] * 5 + [ctypes.POINTER(ctypes.c_int)]
+        L.fa_append_paged_rope.argtypes = ([P] * 8 + [I, I] + [P] * 3 + [I, P, P] + [I] * 13 +
+                                           [F, P])
+        L.fa_append_paged_fp8.argtypes = ([P] * 9 + [I, P, I, I] + [P] * 3 + [I, P, P] +
+                                          [I] * 13 + [F, P])
+        L.fa_decode_paged_fp8.argtypes = ([P] * 5 + [I, P, I, I] + [P] * 3 + [I] * 6 +
+                                          [F, P, I, P])
+        L.fa_decode_paged_fp8_workspace.argtypes = [I] * 4 + [ctypes.POINTER(ctypes.c_int)]
         L.fa_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int), P]
         L.fa_selftest_bounded_wait.argtypes = [P]
         L.fa_selftest_fwd_stall.argtypes = [P, P, P, P, P, I, I, I, I, I, I, P]
@@ -82,6 +98,10 @@ def lib() -> ctypes.CDLL:
                      "fa_decode_paged_gqa", "fa_decode_paged_strided", "fa_decode_paged_noalloc",
                      "fa_append_paged",
                      "fa_prefill_paged", "fa_gather_paged",
+                     "fa_rope_table", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+                     "fa_qk_norm_rope_bwd_workspace", "fa_append_paged_rope",
+                     "fa_append_paged_fp8", "fa_decode_paged_fp8",
+                     "fa_decode_paged_fp8_workspace",
                      "fa_get_device_error", "fa_selftest_bounded_wait", "fa_selftest_fwd_stall",
                      "fa_selftest_decode_stall",
                      "fa_release_workspace", "fa_version", "fa_fwd_set_cta_pairs"):
@@ -561,6 +581,398 @@ def fa_gather_paged(pages, page_table, seq_lens, total_tokens: int, page_size: i
                                out.data_ptr(), B, H, d, int(page_size), _stream(stream))
     _raise_if(rc, "fa_gather_paged")
     return out
+
+
+# ---- rotary tables, norms with the rotation, appends with both, the 8-bit cache ----
+
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "turns": 3, "yarn": 4}
+_FP8 = torch.float8_e4m3fn
+
+
+def _call(name: str, device, stream, *args):
+    """The library's `name` on `stream` (None: the device's current one), with
+    the tensors' device current for the call."""
+    fn = getattr(lib(), name)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the call's inputs on {device}")
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != FA_OK:
+        raise FaError(rc, name)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory of the call's own stream (scratch and outputs may be freed, and
+    handed out again, in that stream's order)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _token_rows(t, name: str, device, shape=None) -> int:
+    """t: bf16 [tokens, heads, d] whose rows [heads, d] are contiguous, tokens
+    any stride apart; returns that stride."""
+    if not isinstance(t, torch.Tensor) or t.device.type not in _DEVICE_TYPES:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {shape or '[tokens, heads, d]'}, got "
+                         f"{tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's inputs on {device}")
+    tokens, heads, d = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and d > 1) or (sh != d and heads > 1):
+        raise ValueError(f"{name}: the [heads, d] part of a token must be contiguous")
+    if tokens <= 1:
+        return heads * d
+    if st < heads * d or st % 8 != 0:
+        raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart, without "
+                         f"overlap; got a stride of {st}")
+    return st
+
+
+def _norm_weights(q_weight, k_weight, d: int, device) -> int:
+    """The weights' type (FA_WEIGHT_*): [d] bf16 or fp32, one type, or None."""
+    dtype = torch.bfloat16
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            dtype = torch.float32 if w.dtype == torch.float32 else torch.bfloat16
+            _expect(w, n, dtype, (d,), device)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise TypeError("q_weight and k_weight must have one type")
+    return int(dtype == torch.float32)
+
+
+def _rope(rope_cos, rope_sin, device):
+    """(max_pos, rotary_dim) of the tables; (0, 0) without them."""
+    if rope_cos is None and rope_sin is None:
+        return 0, 0
+    if rope_cos is None or rope_sin is None:
+        raise ValueError("rope_cos and rope_sin come together")
+    _check(rope_cos, "rope_cos", torch.float32, 2)
+    _expect(rope_sin, "rope_sin", torch.float32, rope_cos.shape, device)
+    if rope_cos.device != device:
+        raise ValueError(f"rope_cos is on {rope_cos.device}, the call's inputs on {device}")
+    return rope_cos.shape[0], 2 * rope_cos.shape[1]
+
+
+def fa_rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                  factor: float = 1.0, original_len: int = 0, low: float = 1.0,
+                  high: float = 4.0, mscale: float = 1.0, rope_cos=None, rope_sin=None,
+                  device=None, stream=None):
+    """Rotary tables (cos, sin), each [max_pos, rotary_dim/2] fp32: mscale times
+    the cosine and sine of p * w_i, with the frequencies w_i = base^(-2i/R)
+    scaled for long contexts: "none", "linear", "ntk", "turns" (blended by the
+    turns within original_len, between low and high) or "yarn" (a ramp over the
+    pairs between them)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+    shape = (int(max_pos), int(rotary_dim) // 2)
+    if shape[0] < 1 or shape[1] < 1 or rotary_dim % 2 != 0:
+        raise ValueError(f"max_pos must be positive and rotary_dim even, got {max_pos}, "
+                         f"{rotary_dim}")
+    if device is None:
+        device = rope_cos.device if rope_cos is not None else \
+            torch.device("cuda", torch.cuda.current_device())
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    if rope_cos is None:
+        rope_cos = _empty(shape, torch.float32, device, stream)
+    if rope_sin is None:
+        rope_sin = _empty(shape, torch.float32, device, stream)
+    _expect(rope_cos, "rope_cos", torch.float32, shape, device)
+    _expect(rope_sin, "rope_sin", torch.float32, shape, device)
+    _call("fa_rope_table", device, stream, rope_cos.data_ptr(), rope_sin.data_ptr(), shape[0],
+          int(rotary_dim), float(base), _SCALINGS[scaling], float(factor), int(original_len),
+          float(low), float(high), float(mscale))
+    return rope_cos, rope_sin
+
+
+def _qk_rows(q, k, positions):
+    """What the calls on queries and keys share: (layout, B, N, H, H_kv, d,
+    stride of q, stride of k), positions checked."""
+    if isinstance(q, torch.Tensor) and q.dim() == 4:
+        _check(q, "q", torch.bfloat16, 4)
+        B, H, N, d = q.shape
+        _check(k, "k", torch.bfloat16, 4)
+        H_kv = k.shape[1]
+        _expect(k, "k", torch.bfloat16, (B, H_kv, N, d), q.device)
+        if positions is not None:
+            _expect(positions, "positions", torch.int32, (B, N), q.device)
+        return 1, B, N, H, H_kv, d, 0, 0
+    q_stride = _token_rows(q, "q", None)
+    k_stride = _token_rows(k, "k", q.device)
+    N, H, d = q.shape
+    if k.shape[0] != N or k.shape[2] != d:
+        raise ValueError(f"k must have q's tokens and d, got {tuple(k.shape)} and "
+                         f"{tuple(q.shape)}")
+    if positions is not None:
+        _expect(positions, "positions", torch.int32, (N,), q.device)
+    return 0, 1, N, H, k.shape[1], d, q_stride, k_stride
+
+
+def _row_arg(t, name: str, like, layout: int, stream):
+    """An output or a gradient of the same shape as `like` and its stride; made
+    contiguous on the call's stream where it is None."""
+    if t is None:
+        return _empty(like.shape, torch.bfloat16, like.device, stream), 0
+    if layout == 1:
+        _expect(t, name, torch.bfloat16, like.shape, like.device)
+        return t, 0
+    return t, _token_rows(t, name, like.device, like.shape)
+
+
+def fa_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope_cos=None, rope_sin=None,
+                    positions=None, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                    k_out=None, stream=None):
+    """Queries and keys normed for each head (weights [d] bf16 or fp32, None: no
+    norm) and rotated (tables [max_pos, R/2] fp32 over the first R values, None:
+    no rotation) in one pass -> (q_out, k_out).  q [tokens,H,d] and k
+    [tokens,H_kv,d] bf16, tokens any stride apart, positions [tokens] int32; or
+    [B,H,N,d] and [B,H_kv,N,d] contiguous, positions [B,N].  No positions:
+    token n is at position n.  The outputs may be the inputs."""
+    layout, B, N, H, H_kv, d, q_st, k_st = _qk_rows(q, k, positions)
+    device = q.device
+    wt = _norm_weights(q_weight, k_weight, d, device)
+    max_pos, rot = _rope(rope_cos, rope_sin, device)
+    q_out, qo_st = _row_arg(q_out, "q_out", q, layout, stream)
+    k_out, ko_st = _row_arg(k_out, "k_out", k, layout, stream)
+    if q.numel() == 0 or k.numel() == 0:
+        if B * N > 0:
+            raise ValueError("q and k need at least one head and value")
+        return q_out, k_out
+    _call("fa_qk_norm_rope", device, stream, q.data_ptr(), k.data_ptr(), q_out.data_ptr(),
+          k_out.data_ptr(), _ptr(q_weight), _ptr(k_weight), wt, _ptr(rope_cos), _ptr(rope_sin),
+          max_pos, rot, int(bool(interleaved)), _ptr(positions), layout, B, N, H, H_kv, d, q_st,
+          k_st, qo_st, ko_st, float(eps))
+    return q_out, k_out
+
+
+def fa_qk_norm_rope_bwd_workspace(B: int, N: int, H: int, H_kv: int, d: int) -> int:
+    """Bytes of scratch of fa_qk_norm_rope_bwd on the current GPU."""
+    n = ctypes.c_int(0)
+    _raise_if(lib().fa_qk_norm_rope_bwd_workspace(B, N, H, H_kv, d, ctypes.byref(n)),
+              "fa_qk_norm_rope_bwd_workspace")
+    return n.value
+
+
+def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope_cos=None,
+                        rope_sin=None, positions=None, eps: float = 1e-6,
+                        interleaved: bool = False, dq=None, dk=None, dq_weight=None,
+                        dk_weight=None, stream=None):
+    """Gradients of fa_qk_norm_rope: (dq, dk, dq_weight, dk_weight) from its
+    inputs and its outputs' gradients; the weights' gradients are fp32 [d], None
+    where there is no weight."""
+    layout, B, N, H, H_kv, d, q_st, k_st = _qk_rows(q, k, positions)
+    device = q.device
+    wt = _norm_weights(q_weight, k_weight, d, device)
+    max_pos, rot = _rope(rope_cos, rope_sin, device)
+    for t, n in ((dq_out, "dq_out"), (dk_out, "dk_out")):
+        if t is None:
+            raise TypeError(f"{n} must be a CUDA tensor")
+    dq_out, gq_st = _row_arg(dq_out, "dq_out", q, layout, stream)
+    dk_out, gk_st = _row_arg(dk_out, "dk_out", k, layout, stream)
+    dq, dq_st = _row_arg(dq, "dq", q, layout, stream)
+    dk, dk_st = _row_arg(dk, "dk", k, layout, stream)
+    grads = []
+    for w, g, n in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
+        if w is None and g is not None:
+            raise ValueError(f"{n} given without its weight")
+        if w is not None and g is None:
+            g = _empty((d,), torch.float32, device, stream)
+        if g is not None:
+            _expect(g, n, torch.float32, (d,), device)
+        grads.append(g)
+    if q.numel() == 0 or k.numel() == 0:
+        if B * N > 0:
+            raise ValueError("q and k need at least one head and value")
+        with torch.cuda.stream(stream):
+            for g in grads:
+                if g is not None:
+                    g.zero_()
+        return dq, dk, grads[0], grads[1]
+    ws = None
+    if q_weight is not None or k_weight is not None:
+        n = _bytes_on(device, "fa_qk_norm_rope_bwd_workspace", B, N, H, H_kv, d)
+        ws = _empty((n,), torch.uint8, device, stream)
+    _call("fa_qk_norm_rope_bwd", device, stream, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(),
+          dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(grads[0]), _ptr(grads[1]),
+          _ptr(q_weight), _ptr(k_weight), wt, _ptr(rope_cos), _ptr(rope_sin), max_pos, rot,
+          int(bool(interleaved)), _ptr(positions), layout, B, N, H, H_kv, d, q_st, k_st, gq_st,
+          gk_st, dq_st, dk_st, float(eps), _ptr(ws), 0 if ws is None else ws.numel())
+    return dq, dk, grads[0], grads[1]
+
+
+def _table(page_table, B: int, device):
+    """(entries, entries of a row) of a packed page table [n] (rows 0) or a
+    block table [B, max_pages]."""
+    if isinstance(page_table, torch.Tensor) and page_table.dim() == 2:
+        _check(page_table, "page_table", torch.int32, 2)
+        if page_table.shape[0] != B:
+            raise ValueError("a block table must have one row per sequence")
+    else:
+        _check(page_table, "page_table", torch.int32, 1)
+    if page_table.device != device:
+        raise ValueError(f"page_table is on {page_table.device}, the call's inputs on {device}")
+    return page_table.numel(), page_table.shape[1] if page_table.dim() == 2 else 0
+
+
+def _append(name, q_new, k_new, v_new, cu_new, k_pages, v_pages, scales, page_table, seq_lens,
+            rope_cos, rope_sin, q_weight, k_weight, eps, interleaved, page_size, q_out, stream):
+    """Checks and call of both appends; `scales`: (k_scales, v_scales) or ()."""
+    k_st = _token_rows(k_new, "k_new", None)
+    device = k_new.device
+    v_st = _token_rows(v_new, "v_new", device, k_new.shape)
+    total, H_kv, d = k_new.shape
+    H, q_st = 0, 0
+    if q_new is not None:
+        q_st = _token_rows(q_new, "q_new", device)
+        H = q_new.shape[1]
+        if q_new.shape != (total, H, d):
+            raise ValueError(f"q_new must have k_new's tokens and d, got {tuple(q_new.shape)}")
+        if q_out is None:
+            q_out = _empty((total, H, d), torch.bfloat16, device, stream)
+        _expect(q_out, "q_out", torch.bfloat16, (total, H, d), device)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q_new")
+    dtype = _FP8 if scales else torch.bfloat16
+    _check(k_pages, "k_pages", dtype, 4)
+    _check(v_pages, "v_pages", dtype, 4)
+    _pages(k_pages, v_pages, page_size, d, heads=H_kv)
+    _check(cu_new, "cu_new", torch.int32, 1)
+    B = cu_new.numel() - 1
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    if seq_lens.numel() != B:
+        raise ValueError("seq_lens must hold one length per sequence of cu_new")
+    _same_device(device, cu_new=cu_new, k_pages=k_pages, v_pages=v_pages, seq_lens=seq_lens)
+    table_len, max_pages = _table(page_table, B, device)
+    block = ()
+    if scales:
+        block = (_scale_block(scales, k_pages, device),)
+    wt = _norm_weights(q_weight, k_weight, d, device)
+    max_pos, rot = _rope(rope_cos, rope_sin, device)
+    if total == 0:
+        return q_out
+    _call(name, device, stream, _ptr(q_new), k_new.data_ptr(), v_new.data_ptr(),
+          cu_new.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(),
+          *(s.data_ptr() for s in scales), *block, page_table.data_ptr() or seq_lens.data_ptr(),
+          table_len, max_pages, seq_lens.data_ptr(), _ptr(q_weight), _ptr(k_weight), wt,
+          _ptr(rope_cos), _ptr(rope_sin), max_pos, rot, int(bool(interleaved)), B, H, H_kv,
+          total, k_pages.shape[0], d, int(page_size), q_st, k_st, v_st, float(eps))
+    return q_out
+
+
+def _scale_block(scales, pages, device) -> int:
+    """Tokens that share a scale: scales [P, H_kv, page_size / block] fp32."""
+    for s, n in zip(scales, ("k_scales", "v_scales")):
+        _check(s, n, torch.float32, 3)
+        if s.device != device:
+            raise ValueError(f"{n} is on {s.device}, the call's inputs on {device}")
+    P, heads, page_size = pages.shape[:3]
+    n = scales[0].shape[2]
+    if scales[1].shape != scales[0].shape or scales[0].shape[:2] != (P, heads) or n < 1 or \
+            page_size % n != 0:
+        raise ValueError(f"scales must be [{P}, {heads}, {page_size} / block], got "
+                         f"{tuple(scales[0].shape)} and {tuple(scales[1].shape)}")
+    return page_size // n
+
+
+def fa_append_paged_rope(q_new, k_new, v_new, cu_new, k_pages, v_pages, page_table, seq_lens,
+                         rope_cos=None, rope_sin=None, q_weight=None, k_weight=None,
+                         eps: float = 1e-6, interleaved: bool = False, page_size: int = 256,
+                         q_out=None, stream=None):
+    """fa_append_paged with the norms and the rotation on the way: new rows
+    [tokens, heads, d] bf16 (any stride between tokens) of sequences cu_new; keys
+    normed, rotated and written to their pages, values written as they are,
+    queries normed and rotated -> q_out (None without q_new).  page_table packed
+    [n] or a block table [B, max_pages]; seq_lens after the append."""
+    return _append("fa_append_paged_rope", q_new, k_new, v_new, cu_new, k_pages, v_pages, (),
+                   page_table, seq_lens, rope_cos, rope_sin, q_weight, k_weight, eps,
+                   interleaved, page_size, q_out, stream)
+
+
+def fa_append_paged_fp8(q_new, k_new, v_new, cu_new, k_pages, v_pages, k_scales, v_scales,
+                        page_table, seq_lens, rope_cos=None, rope_sin=None, q_weight=None,
+                        k_weight=None, eps: float = 1e-6, interleaved: bool = False,
+                        page_size: int = 256, q_out=None, stream=None):
+    """fa_append_paged_rope into pages of torch.float8_e4m3fn values with scales
+    [P, H_kv, 256 / block] fp32, one for each block of tokens and head (updated
+    in place with the pages) -> q_out."""
+    return _append("fa_append_paged_fp8", q_new, k_new, v_new, cu_new, k_pages, v_pages,
+                   (k_scales, v_scales), page_table, seq_lens, rope_cos, rope_sin, q_weight,
+                   k_weight, eps, interleaved, page_size, q_out, stream)
+
+
+def fa_decode_paged_fp8_workspace(B: int, H: int, H_kv: int, d: int) -> int:
+    """Bytes of scratch of fa_decode_paged_fp8 on the current GPU."""
+    n = ctypes.c_int(0)
+    _raise_if(lib().fa_decode_paged_fp8_workspace(B, H, H_kv, d, ctypes.byref(n)),
+              "fa_decode_paged_fp8_workspace")
+    return n.value
+
+
+def fa_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens,
+                        page_size: int = 256, scale: Optional[float] = None, o=None, lse=None,
+                        stream=None):
+    """Decode over the 8-bit cache: q [B,H,d] bf16, pages [P,H_kv,page_size,d]
+    torch.float8_e4m3fn with scales [P,H_kv,page_size/block] fp32, page_table
+    packed [n] or a block table [B, max_pages] -> o [B,H,d] bf16; `lse` [B,H]
+    fp32 is filled where it is given."""
+    _check(q, "q", torch.bfloat16, 3)
+    _check(k_pages, "k_pages", _FP8, 4)
+    _check(v_pages, "v_pages", _FP8, 4)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    B, H, d = q.shape
+    device = q.device
+    _pages(k_pages, v_pages, page_size, d)
+    H_kv = k_pages.shape[1]
+    if H_kv == 0 or H % H_kv != 0:
+        raise ValueError(f"H ({H}) must be a multiple of the cache's K/V heads ({H_kv})")
+    if seq_lens.numel() != B:
+        raise ValueError(f"seq_lens must hold one length per sequence ({B})")
+    _same_device(device, k_pages=k_pages, v_pages=v_pages, seq_lens=seq_lens)
+    block = _scale_block((k_scales, v_scales), k_pages, device)
+    table_len, max_pages = _table(page_table, B, device)
+    if o is None:
+        o = _empty(q.shape, torch.bfloat16, device, stream)
+    _expect(o, "o", torch.bfloat16, q.shape, device)
+    if lse is not None:
+        _expect(lse, "lse", torch.float32, (B, H), device)
+    if q.numel() == 0:
+        return o
+    n = _bytes_on(device, "fa_decode_paged_fp8_workspace", B, H, H_kv, d)
+    ws = _empty((n,), torch.uint8, device, stream) if n else None
+    _call("fa_decode_paged_fp8", device, stream, q.data_ptr(), k_pages.data_ptr(),
+          v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block,
+          page_table.data_ptr() or seq_lens.data_ptr(), table_len, max_pages,
+          seq_lens.data_ptr(), o.data_ptr(), _ptr(lse), B, H, H_kv, k_pages.shape[0], d,
+          int(page_size), d ** -0.5 if scale is None else float(scale), _ptr(ws), n)
+    return o
+
+
+def _bytes_on(device, name: str, *sizes) -> int:
+    """A call's scratch on `device` (what `name` gives there)."""
+    fn, n = getattr(lib(), name), ctypes.c_int(0)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*sizes, ctypes.byref(n))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*sizes, ctypes.byref(n))
+    _raise_if(rc, name)
+    return n.value
 
 
 def fa_get_device_error(stream=None) -> int:

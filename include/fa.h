@@ -417,6 +417,220 @@ FA_API int fa_decode_paged_noalloc(const void* q, const void* k_pages, const voi
                                    const int32_t* page_table, const int32_t* seq_lens, void* o,
                                    int B, int H, int d, int page_size, fa_stream_t stream);
 
+/* Weights of the norms, frequency scalings and row layouts of the calls below. */
+enum fa_weight_type { FA_WEIGHT_BF16 = 0, FA_WEIGHT_FP32 = 1 };
+enum fa_rope_scaling {
+    FA_ROPE_PLAIN = 0,  /* w_i = base^(-2i/R) */
+    FA_ROPE_LINEAR = 1, /* w_i / factor */
+    FA_ROPE_NTK = 2,    /* base * factor^(R/(R-2)) in place of base */
+    FA_ROPE_TURNS = 3,  /* blended by the turns a pair makes within original_len */
+    FA_ROPE_YARN = 4    /* blended over the pairs between two numbers of turns */
+};
+enum fa_layout {
+    FA_LAYOUT_PACKED = 0, /* tokens first: [N, heads, d], a stride between tokens (B = 1) */
+    FA_LAYOUT_HEADS = 1   /* heads first: [B, heads, N, d] contiguous, as fa_fwd takes them */
+};
+
+/*
+ * fa_rope_table -- the sin/cos lookup tables that the rotating calls take
+ * (the page "“Flash”不是那个被时代淘汰的插件" (0539edu.com), section 3, keeps them
+ * precomputed), with the frequencies scaled for contexts longer than a model
+ * was trained on.
+ *   rope_cos, rope_sin : DEVICE fp32 [max_pos, rotary_dim/2] outputs; entry
+ *                        (p, i) = mscale * cos / sin of p * w'_i
+ * With R = rotary_dim (even, 2 .. 256), w_i = base^(-2i/R) and f = factor:
+ *   FA_ROPE_PLAIN   w' = w
+ *   FA_ROPE_LINEAR  w' = w / f
+ *   FA_ROPE_NTK     w' = (base f^(R/(R-2)))^(-2i/R)            (R > 2)
+ *   FA_ROPE_TURNS   a = clamp((original_len w / 2 pi - low) / (high - low), 0, 1),
+ *                   w' = a w + (1 - a) w / f: pairs that turn more than
+ *                   `high` times within original_len stay, those that turn
+ *                   less than `low` times are stretched
+ *   FA_ROPE_YARN    pair(n) = R ln(original_len / (2 pi n)) / (2 ln base),
+ *                   first = max(floor(pair(high)), 0),
+ *                   last = min(ceil(pair(low)), R - 1),
+ *                   a = clamp((i - first) / max(last - first, 0.001), 0, 1),
+ *                   w' = (1 - a) w + a w / f   (low > 0)
+ * The arguments that a scaling does not name are not looked at.  Angles are
+ * formed and reduced in fp64, so far positions keep their accuracy.
+ * Errors: FA_ERR_SHAPE for max_pos < 1, an odd or out-of-range rotary_dim,
+ * base <= 1, factor <= 0, high <= low, original_len < 1, or a value that is
+ * not finite; FA_ERR_UNSUPPORTED for another scaling.
+ */
+FA_API int fa_rope_table(float* rope_cos, float* rope_sin, int max_pos, int rotary_dim,
+                         double base, int scaling, double factor, int original_len, double low,
+                         double high, double mscale, fa_stream_t stream);
+
+/*
+ * fa_qk_norm_rope -- queries and keys normed for each head and rotated by
+ * their positions, in one pass (the rotation of fa_fwd_rope's page and table,
+ * for any layout, position and part of the head).
+ *   y = x * w / sqrt(mean(x^2) + eps)     over the d values of a head
+ *                                         (q_weight / k_weight NULL: y = x)
+ *   then the first R = rotary_dim values of y in pairs: i with i + R/2, or
+ *   2i with 2i + 1 where `interleaved` is non-zero; pair i at position p:
+ *   (a, b) -> (a cos - b sin, b cos + a sin) with entry (p, i) of the tables.
+ * The values from R on stay as they are.  R is a multiple of 16 up to d, or 0
+ * (no rotation; the tables may be NULL).  Everything is computed in fp32 and
+ * rounded once to bf16; products of the rotation are rounded before they are
+ * added, as in fa_fwd_rope.
+ *   q, q_out  : bf16, H heads;  k, k_out : bf16, H_kv heads (any two counts)
+ *   layout    : FA_LAYOUT_PACKED: N tokens (B = 1), rows [heads, d] of
+ *               consecutive tokens *_stride elements apart (0: heads * d; at
+ *               least that, and a multiple of 8), so that q and k may be parts
+ *               of one projection's output.  FA_LAYOUT_HEADS: [B, heads, N, d]
+ *               contiguous, every stride 0
+ *   positions : DEVICE int32, one for each token ([N], or [B, N]); NULL:
+ *               token n is at position n (then max_pos >= N).  A position
+ *               outside [0, max_pos) is reported as FA_ERR_DEVICE_BAD_INPUT
+ *               and its rows are written as zeros
+ *   q_weight, k_weight : DEVICE [d], bf16 or fp32 by weight_type
+ * q_out may be q and k_out may be k, with the same stride.  Needs no workspace.
+ * Errors: FA_ERR_NULL, FA_ERR_ALIGN (a base pointer or a stride),
+ * FA_ERR_SHAPE (sizes, strides, eps < 0, max_pos), FA_ERR_UNSUPPORTED (d,
+ * rotary_dim, layout, weight_type).
+ */
+FA_API int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out,
+                           const void* q_weight, const void* k_weight, int weight_type,
+                           const float* rope_cos, const float* rope_sin, int max_pos,
+                           int rotary_dim, int interleaved, const int32_t* positions, int layout,
+                           int B, int N, int H, int H_kv, int d, int q_stride, int k_stride,
+                           int q_out_stride, int k_out_stride, float eps, fa_stream_t stream);
+
+/*
+ * fa_qk_norm_rope_bwd -- gradients of fa_qk_norm_rope.
+ *   q, k             : its inputs
+ *   dq_out, dk_out   : gradients of its outputs, bf16
+ *   dq, dk           : gradients of q and k, bf16 outputs
+ *   dq_weight,
+ *   dk_weight        : fp32 [d] outputs, gradients of the weights summed over
+ *                      every token and head; NULL exactly where the weight is
+ * With g the output's gradient turned back by the same angles, r = 1/sqrt(
+ * mean(x^2) + eps): dw = sum g x r,  dx = r (g w - x r^2 mean(g w x));
+ * without a weight dx = g.  Sums are in fp32 and, over the CTAs, in fp64, in
+ * a fixed order: the same inputs give the same bits.  A token whose position
+ * is out of range gets zero gradients and adds nothing to the weights'.
+ * Strides, layout, positions, tables, errors as fa_qk_norm_rope.  dq may be
+ * dq_out and dk may be dk_out, with the same stride.
+ *   workspace : DEVICE scratch of at least the bytes that
+ *               fa_qk_norm_rope_bwd_workspace gives (FA_ERR_SHAPE if fewer),
+ *               or NULL: the library's workspace of the stream, which is
+ *               refused (FA_ERR_UNSUPPORTED) while the stream is captured.
+ *               Without weights none is needed
+ */
+FA_API int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out,
+                               const void* dk_out, void* dq, void* dk, float* dq_weight,
+                               float* dk_weight, const void* q_weight, const void* k_weight,
+                               int weight_type, const float* rope_cos, const float* rope_sin,
+                               int max_pos, int rotary_dim, int interleaved,
+                               const int32_t* positions, int layout, int B, int N, int H,
+                               int H_kv, int d, int q_stride, int k_stride, int dq_out_stride,
+                               int dk_out_stride, int dq_stride, int dk_stride, float eps,
+                               void* workspace, int workspace_bytes, fa_stream_t stream);
+
+/* Bytes of scratch that fa_qk_norm_rope_bwd uses for these sizes on the
+ * current GPU. */
+FA_API int fa_qk_norm_rope_bwd_workspace(int B, int N, int H, int H_kv, int d, int* bytes);
+
+/*
+ * fa_append_paged_rope -- fa_append_paged with the norms and the rotation on
+ * the way: one launch from the projections' output to what attention reads.
+ *   q_new  : [total_new, H, d] bf16 or NULL;  q_out : [total_new, H, d] bf16
+ *            contiguous, the queries normed and rotated (NULL with q_new)
+ *   k_new, v_new : [total_new, H_kv, d] bf16; keys are normed and rotated and
+ *            written to k_pages, values written to v_pages as they are
+ *   q_stride, k_stride, v_stride : elements between tokens (0: heads * d; at
+ *            least that, a multiple of 8)
+ *   cu_new, k_pages, v_pages, seq_lens : as fa_append_paged
+ *   page_table : int32; max_pages = 0: packed, as fa_append_paged, table_len
+ *            entries; max_pages > 0: a block table, max_pages entries for each
+ *            sequence (table_len >= B * max_pages)
+ *   q_weight, k_weight, weight_type, rope_cos, rope_sin, max_pos, rotary_dim,
+ *   interleaved, eps : as fa_qk_norm_rope; a token's position is its place in
+ *            the cache, seq_lens[b] - n_b + i
+ * A sequence with more new rows than tokens, longer than max_pos (with a
+ * rotation), or with more pages than its table holds is reported as
+ * FA_ERR_DEVICE_BAD_INPUT: its q_out rows are zeros and nothing of it is
+ * stored.  Offsets outside [0, total_new] and page indices outside
+ * [0, num_pages) are reported and skipped.  Rows that no sequence holds are
+ * left as they were, in q_out too.  Pages being written must belong to one
+ * sequence each (a shared page's new rows would be written twice, in either
+ * order).  page_size must be 256.  Needs no workspace.
+ */
+FA_API int fa_append_paged_rope(const void* q_new, const void* k_new, const void* v_new,
+                                const int32_t* cu_new, void* q_out, void* k_pages, void* v_pages,
+                                const int32_t* page_table, int table_len, int max_pages,
+                                const int32_t* seq_lens, const void* q_weight,
+                                const void* k_weight, int weight_type, const float* rope_cos,
+                                const float* rope_sin, int max_pos, int rotary_dim,
+                                int interleaved, int B, int H, int H_kv, int total_new,
+                                int num_pages, int d, int page_size, int q_stride, int k_stride,
+                                int v_stride, float eps, fa_stream_t stream);
+
+/*
+ * fa_append_paged_fp8 -- fa_append_paged_rope into a cache of 8-bit values
+ * (e4m3: 4 exponent and 3 mantissa bits, largest 448, no infinity) with one
+ * scale for each block of tokens and head.
+ *   k_pages, v_pages   : [num_pages, H_kv, 256, d], one byte a value
+ *   k_scales, v_scales : fp32 [num_pages, H_kv, 256 / block]; the value stored
+ *                        is code * scale of the token's block
+ *   block : tokens that share a scale: 16, 32, 64, 128 or 256
+ * Keys (after norm and rotation, in fp32) and values are divided by their
+ * block's scale and rounded once, to nearest even.  With a the largest finite
+ * magnitude among a block's new values, its scale is the least power of two s
+ * with a <= 448 s (2^-64 .. 2^64); a block that already holds tokens of the
+ * sequence takes the larger of that and its present scale, and its codes are
+ * rounded again when the scale grows (exact for power-of-two scales, but for
+ * codes that fall below 2^-6).  Infinities, NaN and magnitudes beyond
+ * 448 * 2^64 are stored as NaN.  Present scales must be positive and finite.
+ * Everything else as fa_append_paged_rope; a block whose page index is out of
+ * range is skipped.  block outside the list: FA_ERR_UNSUPPORTED.
+ */
+FA_API int fa_append_paged_fp8(const void* q_new, const void* k_new, const void* v_new,
+                               const int32_t* cu_new, void* q_out, void* k_pages, void* v_pages,
+                               float* k_scales, float* v_scales, int block,
+                               const int32_t* page_table, int table_len, int max_pages,
+                               const int32_t* seq_lens, const void* q_weight,
+                               const void* k_weight, int weight_type, const float* rope_cos,
+                               const float* rope_sin, int max_pos, int rotary_dim,
+                               int interleaved, int B, int H, int H_kv, int total_new,
+                               int num_pages, int d, int page_size, int q_stride, int k_stride,
+                               int v_stride, float eps, fa_stream_t stream);
+
+/*
+ * fa_decode_paged_fp8 -- single-token decode over the 8-bit cache that
+ * fa_append_paged_fp8 fills: fa_decode_paged_gqa with k = code * k_scale and
+ * v = code * v_scale.
+ *   q, o     : [B, H, d] bf16
+ *   k_pages, v_pages, k_scales, v_scales, block : as fa_append_paged_fp8; any
+ *              scales that are 0 or within [2^-64, 2^64] (not only powers of
+ *              two); slots and scales behind a sequence's last token may hold
+ *              anything
+ *   page_table, table_len, max_pages : as fa_append_paged_rope
+ *   seq_lens : [B] int32; 0 gives o = 0 (lse = -inf); a negative entry is
+ *              treated as 0 and reported as FA_ERR_DEVICE_BAD_INPUT
+ *   lse      : NULL, or fp32 [B, H]: natural log of the sum of exponentials
+ *   scale    : softmax scale (normally 1/sqrt(d))
+ * H is any multiple of H_kv; query head h reads K/V head h / (H / H_kv).  A
+ * sequence longer than its table's entries is reported and cut to them; a page
+ * index outside [0, num_pages) is reported and that sequence's output is
+ * unspecified (nothing outside the pool is read).
+ *   workspace : DEVICE scratch of at least the bytes that
+ *               fa_decode_paged_fp8_workspace gives, or NULL, as
+ *               fa_qk_norm_rope_bwd.  Calls that may overlap on the GPU need
+ *               one each
+ */
+FA_API int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
+                               const float* k_scales, const float* v_scales, int block,
+                               const int32_t* page_table, int table_len, int max_pages,
+                               const int32_t* seq_lens, void* o, float* lse, int B, int H,
+                               int H_kv, int num_pages, int d, int page_size, float scale,
+                               void* workspace, int workspace_bytes, fa_stream_t stream);
+
+/* Bytes of scratch that fa_decode_paged_fp8 uses for these sizes on the
+ * current GPU (whatever the lengths). */
+FA_API int fa_decode_paged_fp8_workspace(int B, int H, int H_kv, int d, int* bytes);
+
 /*
  * fa_get_device_error -- synchronise `stream`, then read and clear the
  * current GPU's device error word.  *code receives FA_OK or the FA_ERR_*
