@@ -1,7 +1,42 @@
 // decode_fp8_sm100.cu -- single-token decode over a paged cache of 8-bit
 // values (e4m3) with one scale for each block of tokens and head.
-#include <cuda_fp8.h>
-
+//
+// The cache is the page pool of the page "“Flash”不是那个被时代淘汰的插件"
+// (0539edu.com), section 2, which notes that decode is bound by memory
+// traffic: at 8 bits there is half of it, and twice the arithmetic for each
+// byte.  For one sequence and K/V head, with the G query heads that share it,
+//     s[g, l] = scale * q[g] . kcode[l] * kscale(l),   p = 2^(s log2 e - m),
+//     o[g] = sum_l p[g, l] vscale(l) vcode[l] / sum_l p[g, l],
+// the running maximum m as in the page "Flash Attention 是什么", section
+// 关键术语解析, item 4.
+//
+// Two launches: split and merge.  The tokens of all sequences and K/V heads
+// form one stream of 32-token tiles, and each warp of a grid that fills the
+// GPU takes an equal, contiguous piece of it, whatever the lengths.  A warp
+// that holds all of a sequence's head writes the output; pieces of one that is
+// cut are written as normalised partial outputs with their log-sum-exp, which
+// the second launch joins.  There is no plan kernel: each CTA sums the lengths
+// itself while it starts.
+//
+// Within a warp nothing goes through shared memory but the query.  The matrix
+// instruction's first operand is the cache: S^T[tokens, heads] = K Q^T and
+// O^T[d, heads] += V^T P^T, m16n8k16 in fp16 with fp32 sums, to which the
+// conversion from e4m3 is exact.  The order of d in the first product and of d
+// in the rows of the second is free, and is chosen so that each lane's share
+// of a fragment is 16 consecutive bytes of a token: K and V go from global
+// memory to registers in whole 128-byte rows, 8 KB a warp in flight, and only
+// V's bytes are paired across two tokens (a byte permute).  S^T's accumulators
+// are P^T's operand after one 8 x 8 transpose in registers.  8 query heads
+// fill an instruction's 8 columns; up to 16 take two of them, more are split
+// into groups that neighbouring warps run side by side over the same tokens.
+// (With the heads in the 16 rows instead, 8 heads would leave half of every
+// instruction and half of the accumulators empty.)
+//
+// Rounding: each query row is scaled by a power of two into fp16, which holds
+// its 8 bits exactly; scores, maxima and sums are fp32; weights p * vscale are
+// rounded to fp16 (11 bits), scaled by a power of two that follows the largest
+// value scale so far, so that block scales may differ by 2^28 before small
+// ones lose bits.
 #include <cmath>
 
 #include "fa_internal.h"
@@ -11,7 +46,10 @@ namespace fa {
 namespace {
 
 constexpr int kPage = 256;
-constexpr int kThreads = 128;
+constexpr int kTile = 32;  // tokens a step of a warp
+constexpr int kWarps = 4;  // a CTA
+constexpr int kThreads = kWarps * 32;
+constexpr int kMergeThreads = 128;
 
 struct DecodeFp8 {
     const __nv_bfloat16* q;
@@ -20,88 +58,621 @@ struct DecodeFp8 {
     const int32_t *table, *lens;
     __nv_bfloat16* o;
     float* lse;
-    int B, H, Hk, num_pages, table_len, max_pages, block_log2;
+    float *part_o, *part_lse;  // [2 * warps, 8 * NT (, D)] pieces
+    int B, H, Hk, G, num_pages, table_len, max_pages, block_log2;
+    int groups, group_heads;  // groups of query heads of one K/V head
+    int ranges;               // warps of each group: the stream's ranges, at most
     float scale_log2;
     unsigned int* err;
 };
 
-__device__ __forceinline__ float code_value(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
-// One CTA per (sequence, query head); 128 tokens at a time: a thread scores
-// one token, then sums one output column (two threads' share for D = 64).
-template <int D>
-__global__ void __launch_bounds__(kThreads) fa_decode_fp8_kernel(const DecodeFp8 p) {
-    __shared__ float q[D], prob[kThreads], red[kThreads / 32];
-    __shared__ unsigned long long base_sh;
-    const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H, hk = h / (p.H / p.Hk);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < D) q[tid] = __bfloat162float(p.q[(static_cast<int64_t>(b) * p.H + h) * D + tid]) * p.scale_log2;
-    if (tid == 0) base_sh = 0;
-    __syncthreads();
-    int len = max(p.lens[b], 0);
-    if (p.max_pages == 0) {
-        unsigned long long mine = 0;
-        for (int i = tid; i < b; i += kThreads) {
-            const int n = max(p.lens[i], 0);
-            mine += n / kPage + (n % kPage != 0);
-        }
-        if (mine) atomicAdd(&base_sh, mine);
-    }
-    if (p.lens[b] < 0 && tid == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
-    __syncthreads();
-    const int64_t base = p.max_pages ? static_cast<int64_t>(b) * p.max_pages
-                                     : static_cast<int64_t>(base_sh);
-    const int64_t room = p.max_pages ? p.max_pages : p.table_len > base ? p.table_len - base : 0;
+// ---- the stream of tiles ------------------------------------------------------
+// Sequence b's cached tokens as its length and its table's entries give them,
+// the first entry at `base` (lengths may be anything: 64-bit sums).
+__device__ __forceinline__ int usable_len(const DecodeFp8& p, int len, int64_t base, bool& bad) {
+    bad = len < 0;
+    if (len <= 0) return 0;
+    const int64_t room = p.max_pages ? p.max_pages : max(int64_t{0}, p.table_len - base);
     if (len > room * kPage) {
-        if (tid == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
+        bad = true;
         len = static_cast<int>(room * kPage);
     }
-    float m = -INFINITY, l = 0.f, acc = 0.f;
-    for (int t0 = 0; t0 < len; t0 += kThreads) {
-        int page = p.table[base + t0 / kPage];
-        if (page < 0 || page >= p.num_pages) {
-            if (tid == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
-            page = 0;
+    return len;
+}
+__device__ __forceinline__ int pages_of(int len) {
+    return len <= 0 ? 0 : len / kPage + (len % kPage != 0);
+}
+__device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
+
+// One sequence a thread: its table base, usable length and the tiles before it.
+struct Slice {
+    int64_t base, tiles_before;
+    int len;
+};
+
+struct ScanShared {
+    int64_t sum[kWarps];
+};
+
+// Exclusive prefix over the block of one value a thread; `total` of the block.
+__device__ __forceinline__ int64_t block_prefix(int64_t v, ScanShared& sh, int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t n = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += n;
+    }
+    if (lane == 31) sh.sum[warp] = inc;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) inc += sh.sum[w];
+        total += sh.sum[w];
+    }
+    __syncthreads();
+    return inc - v;
+}
+
+// Sequences first .. first + kThreads - 1, with the pages and tiles before them.
+__device__ __forceinline__ Slice scan_chunk(const DecodeFp8& p, int first, int64_t& pages,
+                                            int64_t& tiles, ScanShared& sh) {
+    const int i = first + threadIdx.x;
+    const int len = i < p.B ? __ldg(p.lens + i) : 0;
+    Slice s;
+    int64_t total = 0;
+    if (p.max_pages) {
+        s.base = static_cast<int64_t>(i) * p.max_pages;
+    } else {
+        s.base = pages + block_prefix(pages_of(len), sh, total);
+        pages += total;
+    }
+    bool bad;
+    s.len = usable_len(p, len, s.base, bad);
+    if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
+    s.tiles_before = tiles + block_prefix(tiles_of(s.len), sh, total);
+    tiles += total;
+    return s;
+}
+
+// The stream is cut into as many ranges as there are warps, but no empty ones.
+__device__ __forceinline__ int ranges_of(const DecodeFp8& p, int64_t T) {
+    return static_cast<int>(min(static_cast<int64_t>(p.ranges), T));
+}
+// Range r of `ranges` equal ones of T tiles, and the range that holds tile t.
+__device__ __forceinline__ int64_t range_start(int64_t r, int64_t T, int ranges) {
+    return r * T / ranges;
+}
+__device__ __forceinline__ int64_t range_of(int64_t t, int64_t T, int ranges) {
+    return ((t + 1) * ranges - 1) / T;
+}
+
+// ---- fragments ------------------------------------------------------------------
+__device__ __forceinline__ void cvt4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Cache bytes are read once: kept out of L1, and in the order written here.
+template <int N>
+__device__ __forceinline__ void load_bytes(uint32_t (&r)[N], const uint8_t* p) {
+    static_assert(N == 4 || N == 2, "16 or 8 bytes");
+    if constexpr (N == 4)
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "l"(p));
+    else
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                     : "=r"(r[0]), "=r"(r[1])
+                     : "l"(p));
+}
+
+// Where a warp is in the stream.
+struct Cursor {
+    int b, hk, len, tile, tiles;
+    int64_t base;   // of the sequence's table entries
+    int64_t slice;  // (page, head) of the tile, in slices of kPage tokens
+    int ahead;      // the next page's index
+};
+
+__device__ __forceinline__ int page_index(const DecodeFp8& p, const Cursor& c, int k) {
+    int page = __ldg(p.table + c.base + k);
+    if (page < 0 || page >= p.num_pages) {
+        record_error(p.err, FA_DEVERR_BAD_INPUT);
+        page = 0;
+    }
+    return page;
+}
+
+// The cursor's page, and the one after it (of the same sequence) on its way.
+__device__ __forceinline__ void enter_head(const DecodeFp8& p, Cursor& c) {
+    const int k = c.tile / (kPage / kTile);
+    c.slice = static_cast<int64_t>(page_index(p, c, k)) * p.Hk + c.hk;
+    c.ahead = k < (c.len - 1) / kPage ? page_index(p, c, k + 1) : 0;
+}
+
+__device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
+    if (++c.tile < c.tiles) {
+        if (c.tile % (kPage / kTile) == 0) {
+            c.slice = static_cast<int64_t>(c.ahead) * p.Hk + c.hk;
+            const int k = c.tile / (kPage / kTile);
+            c.ahead = k < (c.len - 1) / kPage ? page_index(p, c, k + 1) : 0;
         }
-        const int64_t slice = static_cast<int64_t>(page) * p.Hk + hk;
-        const int t = t0 + tid, slot = t % kPage, nb = kPage >> p.block_log2;
-        float s = -INFINITY;
-        if (t < len) {
-            s = 0.f;
-            const uint8_t* k = p.kp + (slice * kPage + slot) * D;
-            for (int c = 0; c < D; ++c) s += q[c] * code_value(k[c]);
-            s *= p.ks[slice * nb + (slot >> p.block_log2)];
-        }
-        float top = s;
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) red[warp] = top;
-        __syncthreads();
-        for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, red[i]);
-        const float m2 = fmaxf(m, top), old = exp2f(m - m2);
-        m = m2;
-        prob[tid] = t < len ? exp2f(s - m2) : 0.f;
-        __syncthreads();
-        acc *= old;
-        l *= old;
-        const int n = min(kThreads, len - t0);
-        for (int i = 0; i < n; ++i) {
-            l += prob[i];
-            if (tid < D) {
-                const int sl = (t0 + i) % kPage;
-                acc += prob[i] * p.vs[slice * nb + (sl >> p.block_log2)] *
-                       code_value(p.vp[(slice * kPage + sl) * D + tid]);
+        return;
+    }
+    c.tile = 0;
+    if (++c.hk == p.Hk) {
+        c.hk = 0;
+        do {  // the caller has tiles left, so there is such a sequence
+            c.base = p.max_pages ? c.base + p.max_pages : c.base + pages_of(__ldg(p.lens + c.b));
+            ++c.b;
+            bool bad;
+            c.len = usable_len(p, __ldg(p.lens + c.b), c.base, bad);
+        } while (c.len == 0 && c.b + 1 < p.B);
+        c.tiles = tiles_of(c.len);
+    }
+    enter_head(p, c);
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+    fa_decode_fp8_split_kernel(const DecodeFp8 p) {
+    constexpr int KJ = D / 64;   // 16-byte loads of a token's K for each lane
+    constexpr int VW = D / 32;   // words of a token's V for each lane
+    constexpr int MT = D / 16;   // 16-row tiles of O^T
+    __shared__ ScanShared scan;
+    __shared__ Slice found[kWarps];
+    __shared__ int found_b[kWarps];
+    __shared__ uint4 qs[kWarps][NT][2 * KJ][32];  // query fragments, a lane's own
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;");
+
+    int64_t pages = 0, tiles = 0;
+    Slice s = scan_chunk(p, 0, pages, tiles, scan);
+    for (int first = kThreads; first < p.B; first += kThreads)
+        scan_chunk(p, first, pages, tiles, scan);
+    const int64_t T = tiles * p.Hk;
+    if (T == 0) return;
+    const int ranges = ranges_of(p, T);
+    // consecutive ranges on different CTAs, so that a few spread over the SMs
+    const int wid = warp * gridDim.x + blockIdx.x;
+    const int r = wid / p.groups, group = wid - r * p.groups;
+    pages = tiles = 0;
+    for (int first = 0; first < p.B; first += kThreads) {
+        if (p.B > kThreads) s = scan_chunk(p, first, pages, tiles, scan);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const int64_t at =
+                range_start((w * gridDim.x + blockIdx.x) / p.groups, T, ranges);
+            if (at >= s.tiles_before * p.Hk && at < (s.tiles_before + tiles_of(s.len)) * p.Hk) {
+                found[w] = s;
+                found_b[w] = first + threadIdx.x;
             }
         }
-        __syncthreads();
     }
+    __syncthreads();
+    if (r >= ranges) return;
+    const int64_t start = range_start(r, T, ranges);
+    int64_t left = range_start(r + 1, T, ranges) - start;
+
+    Cursor c;
+    c.b = found_b[warp];
+    c.len = found[warp].len;
+    c.base = found[warp].base;
+    c.tiles = tiles_of(c.len);
+    const int64_t in_seq = start - found[warp].tiles_before * p.Hk;
+    c.hk = static_cast<int>(in_seq / c.tiles);
+    c.tile = static_cast<int>(in_seq - static_cast<int64_t>(c.hk) * c.tiles);
+    enter_head(p, c);
+
+    const int heads = min(p.group_heads, p.G - group * p.group_heads);  // of this group
+    const int nb_log2 = 8 - p.block_log2;  // blocks of a page
+    uint32_t kr[2][2][KJ][4], vr[2][4][VW];
+    float ks[2], vs[2];
+    auto load_k = [&](const Cursor& x) {
+        const int slot0 = (x.tile * kTile) % kPage, last = slot0 + x.len - 1 - x.tile * kTile;
+        const uint8_t* base = p.kp + x.slice * (kPage * D) + 16 * t;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            ks[m] = __ldg(p.ks + (x.slice << nb_log2) + (min(slot0 + 16 * m, last) >> p.block_log2));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                // behind the last token: that token again
+                const uint8_t* row = base + min(slot0 + 16 * m + 8 * h + g, last) * D;
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) load_bytes(kr[m][h][j], row + 64 * j);
+            }
+        }
+    };
+    auto load_v = [&](const Cursor& x) {
+        const int slot0 = (x.tile * kTile) % kPage, last = slot0 + x.len - 1 - x.tile * kTile;
+        const uint8_t* base = p.vp + x.slice * (kPage * D) + D / 8 * g;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            vs[m] = __ldg(p.vs + (x.slice << nb_log2) + (min(slot0 + 16 * m, last) >> p.block_log2));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                load_bytes(vr[m][i],
+                           base + min(slot0 + 16 * m + 2 * t + (i & 1) + 8 * (i >> 1), last) * D);
+        }
+    };
+
+    float o[NT][MT][4], m_run[NT][2], l_run[NT][2], fac[NT][2];
+    float v_top = 0.f;  // power of two, at least every value scale so far
+    // A new head of a sequence: its queries as fragments, and an empty state.
+    auto begin = [&](int b, int hk) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int hh = nt * 8 + g;
+            const bool real = hh < heads;
+            const __nv_bfloat16* row =
+                p.q + (static_cast<int64_t>(b) * p.H + hk * p.G + group * p.group_heads +
+                       (real ? hh : 0)) * D;
+            float x[KJ][16], top = 0.f;
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                const uint4* src = reinterpret_cast<const uint4*>(row + 64 * j + 16 * t);
+                float y[8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    unpack8(__ldg(src + h), y);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        x[j][8 * h + i] = real ? y[i] : 0.f;
+                        top = fmaxf(top, fabsf(x[j][8 * h + i]));
+                    }
+                }
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // times 2^(14 - floor(log2 top)), no more than 2^126
+            const uint32_t e = min(268u - (__float_as_uint(top) >> 23), 253u);
+            const float up = __uint_as_float(e << 23);
+            const float f = p.scale_log2 * __uint_as_float((254u - e) << 23);
+            fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+            fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+#pragma unroll
+            for (int j = 0; j < KJ; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    qs[warp][nt][2 * j + h][lane] =
+                        make_uint4(pack_f16x2(x[j][8 * h] * up, x[j][8 * h + 1] * up),
+                                   pack_f16x2(x[j][8 * h + 2] * up, x[j][8 * h + 3] * up),
+                                   pack_f16x2(x[j][8 * h + 4] * up, x[j][8 * h + 5] * up),
+                                   pack_f16x2(x[j][8 * h + 6] * up, x[j][8 * h + 7] * up));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m_run[nt][i] = -INFINITY;
+                l_run[nt][i] = 0.f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.f;
+        }
+        v_top = 0x1p-64f;
+    };
+
+    load_k(c);
+    load_v(c);
+    begin(c.b, c.hk);
+    bool whole = c.tile == 0, first_piece = true;
+    while (true) {
+        const int b = c.b, hk = c.hk, tok0 = c.tile * kTile, len = c.len;
+        const bool seg_end = c.tile + 1 == c.tiles, more = left > 1;
+        --left;
+        if (more) advance(p, c);
+        // ---- S^T = K Q^T -------------------------------------------------------
+        float sc[NT][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sc[nt][m][i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint4 qf[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) qf[nt] = qs[warp][nt][2 * j + h][lane];
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint32_t a0, a1, a2, a3;
+                        cvt4(kr[m][0][j][2 * h + s2], a0, a2);
+                        cvt4(kr[m][1][j][2 * h + s2], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma_f16(sc[nt][m], a0, a1, a2, a3, s2 ? qf[nt].z : qf[nt].x,
+                                    s2 ? qf[nt].w : qf[nt].y);
+                    }
+                }
+            }
+        }
+        const float k0 = ks[0], k1 = ks[1], v0 = vs[0], v1 = vs[1];
+        if (more) load_k(c);
+        // ---- softmax over the tile's tokens ---------------------------------------
+        const float v_new = fmaxf(
+            v_top, __uint_as_float((max(__float_as_uint(v0), __float_as_uint(v1)) + 0x7fffffu) &
+                                   0x7f800000u));
+        // 2^15 / v_new
+        const float up = __uint_as_float((269u << 23) - __float_as_uint(v_new));
+        const float w0 = v0 * up, w1 = v1 * up;
+        bool moved = v_new != v_top;
+        float keep[NT][2];
+        uint32_t pf[NT][2][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sc[nt][m][i] = sc[nt][m][i] * fac[nt][i & 1] * (m ? k1 : k0);
+                    if (tok0 + 16 * m + 8 * (i >> 1) + g >= len) sc[nt][m][i] = -INFINITY;
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float top = fmaxf(fmaxf(sc[nt][0][i], sc[nt][0][i + 2]),
+                                  fmaxf(sc[nt][1][i], sc[nt][1][i + 2]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                const float m_new = fmaxf(m_run[nt][i], top);
+                const float base = m_new == -INFINITY ? 0.f : m_new;
+                keep[nt][i] = ex2_approx(m_run[nt][i] - base);
+                moved = moved || m_new != m_run[nt][i];
+                m_run[nt][i] = m_new;
+                float sum = 0.f;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float& x = sc[nt][m][i + 2 * h];
+                        x = ex2_approx(x - base);
+                        sum += x;
+                    }
+                l_run[nt][i] = l_run[nt][i] * keep[nt][i] + sum;
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    pf[nt][m][h] = transpose8x8(pack_f16x2(sc[nt][m][2 * h] * (m ? w1 : w0),
+                                                           sc[nt][m][2 * h + 1] * (m ? w1 : w0)));
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+            const float down = v_top / v_new;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float k_0 = keep[nt][0] * down, k_1 = keep[nt][1] * down;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    o[nt][mt][0] *= k_0;
+                    o[nt][mt][1] *= k_1;
+                    o[nt][mt][2] *= k_0;
+                    o[nt][mt][3] *= k_1;
+                }
+            }
+            v_top = v_new;
+        }
+        // ---- O^T += V^T P^T ----------------------------------------------------------
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                    uint32_t a0, a1, a2, a3;
+                    cvt4(__byte_perm(vr[m][0][w], vr[m][1][w], hi ? 0x7362 : 0x5140), a0, a1);
+                    cvt4(__byte_perm(vr[m][2][w], vr[m][3][w], hi ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(o[nt][2 * w + hi], a0, a1, a2, a3, pf[nt][m][0], pf[nt][m][1]);
+                }
+            }
+        }
+        if (more) load_v(c);
+        if (!seg_end && more) continue;
+        // ---- the end of a head, or of the warp's range ------------------------------
+        whole = whole && seg_end;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float l = l_run[nt][i];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                const int hh = nt * 8 + 2 * t + i;
+                if (hh >= heads) continue;
+                const float lse2 = m_run[nt][i] + log2f(l);
+                const float inv = (l == 0.f ? 0.f : 1.f / l) * (v_top * 0x1p-15f);
+                if (whole) {
+                    const int64_t row =
+                        static_cast<int64_t>(b) * p.H + hk * p.G + group * p.group_heads + hh;
+                    if (p.lse && g == 0) p.lse[row] = lse2 * 0.69314718055994531f;
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + D / 8 * g);
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt += 4)
+                        *reinterpret_cast<uint4*>(dst + mt) = make_uint4(
+                            pack_bf16x2(o[nt][mt][i] * inv, o[nt][mt][i + 2] * inv),
+                            pack_bf16x2(o[nt][mt + 1][i] * inv, o[nt][mt + 1][i + 2] * inv),
+                            pack_bf16x2(o[nt][mt + 2][i] * inv, o[nt][mt + 2][i + 2] * inv),
+                            pack_bf16x2(o[nt][mt + 3][i] * inv, o[nt][mt + 3][i + 2] * inv));
+                } else {
+                    const int64_t slot =
+                        (2 * static_cast<int64_t>(wid) + !first_piece) * (8 * NT) + hh;
+                    if (g == 0) p.part_lse[slot] = lse2;
+                    float* dst = p.part_o + slot * D + D / 8 * g;
+#pragma unroll
+                    for (int mt = 0; mt < MT; mt += 2)
+                        *reinterpret_cast<float4*>(dst + 2 * mt) =
+                            make_float4(o[nt][mt][i] * inv, o[nt][mt][i + 2] * inv,
+                                        o[nt][mt + 1][i] * inv, o[nt][mt + 1][i + 2] * inv);
+                }
+            }
+        }
+        if (!more) return;
+        whole = true;
+        first_piece = false;
+        begin(c.b, c.hk);
+    }
+}
+
+// One (sequence, query head) a CTA: the pieces of a head that the ranges cut,
+// o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M); and what has no tokens.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) fa_decode_fp8_merge_kernel(const DecodeFp8 p,
+                                                                            int slots) {
+    static_assert(kMergeThreads == kThreads, "the scan's block");
+    constexpr int V = D / 32;
+    __shared__ ScanShared scan;
+    __shared__ Slice mine_sh;
+    __shared__ float red[kWarps], acc_sh[kWarps][D], w_sh[kWarps];
+    const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t pages = 0, tiles = 0;
+    for (int first = 0; first < p.B; first += kThreads) {
+        const Slice s = scan_chunk(p, first, pages, tiles, scan);
+        if (first + static_cast<int>(threadIdx.x) == b) mine_sh = s;
+    }
+    __syncthreads();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = static_cast<int64_t>(b) * p.H + h;
-    if (tid < D) p.o[row * D + tid] = __float2bfloat16(len > 0 ? acc / l : 0.f);
-    if (tid == 0 && p.lse) p.lse[row] = len > 0 ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    const int n = tiles_of(mine_sh.len);
+    if (n == 0) {
+        if (threadIdx.x < D) p.o[row * D + threadIdx.x] = __float2bfloat16(0.f);
+        if (threadIdx.x == 0 && p.lse) p.lse[row] = -INFINITY;
+        return;
+    }
+    const int hk = h / p.G, hg = h - hk * p.G, group = hg / p.group_heads;
+    const int hh = hg - group * p.group_heads;
+    const int64_t T = tiles * p.Hk, t0 = mine_sh.tiles_before * p.Hk + static_cast<int64_t>(hk) * n;
+    const int ranges = ranges_of(p, T);
+    const int64_t r0 = range_of(t0, T, ranges), r1 = range_of(t0 + n - 1, T, ranges);
+    if (r0 == r1) return;  // the warp wrote it
+    const int pieces = static_cast<int>(r1 - r0) + 1;
+    const bool from_start = range_start(r0, T, ranges) == t0;
+    auto slot = [&](int i) {
+        const int64_t w = (r0 + i) * p.groups + group;
+        return (2 * w + (i == 0 && !from_start)) * slots + hh;
+    };
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < pieces; i += kMergeThreads)
+        top = fmaxf(top, p.part_lse[slot(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[w]);
+    if (top == -INFINITY) top = 0.f;
+    float acc[V], sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+#pragma unroll 4
+    for (int i = warp; i < pieces; i += kWarps) {
+        const int64_t s = slot(i);
+        const float w = ex2_approx(p.part_lse[s] - top);
+        const float* src = p.part_o + s * D + V * lane;
+        sum += w;
+        if constexpr (V == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            acc[0] = fmaf(w, x.x, acc[0]);
+            acc[1] = fmaf(w, x.y, acc[1]);
+            acc[2] = fmaf(w, x.z, acc[2]);
+            acc[3] = fmaf(w, x.w, acc[3]);
+        } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            acc[0] = fmaf(w, x.x, acc[0]);
+            acc[1] = fmaf(w, x.y, acc[1]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc_sh[warp][V * lane + j] = acc[j];
+    if (lane == 0) w_sh[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float a = 0.f, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            a += acc_sh[w][threadIdx.x];
+            l += w_sh[w];
+        }
+        p.o[row * D + threadIdx.x] = __float2bfloat16(l == 0.f ? 0.f : a / l);
+        if (threadIdx.x == 0 && p.lse) p.lse[row] = (top + log2f(l)) * 0.69314718055994531f;
+    }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// How the query heads of a K/V head and the warps are cut.
+struct Shape {
+    int groups, group_heads, nt, ctas, ranges;
+    size_t lse_bytes, bytes;
+};
+
+Shape shape_of(int H, int H_kv, int d, int num_sms) {
+    Shape s;
+    const int G = H / H_kv;
+    s.groups = (G + 15) / 16;
+    s.group_heads = (G + s.groups - 1) / s.groups;
+    s.nt = s.group_heads > 8 ? 2 : 1;
+    s.ctas = num_sms * (s.nt == 1 ? 3 : 2);
+    const int min_ctas = (s.groups + kWarps - 1) / kWarps;
+    if (s.ctas < min_ctas) s.ctas = min_ctas;  // a warp for each group
+    s.ranges = s.ctas * kWarps / s.groups;
+    const size_t rows = static_cast<size_t>(s.ctas) * kWarps * 2 * 8 * s.nt;
+    s.lse_bytes = (rows * sizeof(float) + 255) & ~size_t{255};
+    s.bytes = s.lse_bytes + rows * d * sizeof(float);
+    return s;
+}
+
+template <int D>
+int launch(const DecodeFp8& p, const Shape& s, cudaStream_t st) {
+    if (s.nt == 1) fa_decode_fp8_split_kernel<D, 1><<<s.ctas, kThreads, 0, st>>>(p);
+    else fa_decode_fp8_split_kernel<D, 2><<<s.ctas, kThreads, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.H);
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa_decode_fp8_merge_kernel<D>, p, 8 * s.nt) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
+}
 
 }  // namespace
 }  // namespace fa
@@ -112,7 +683,12 @@ int fa_decode_paged_fp8_workspace(int B, int H, int H_kv, int d, int* bytes) {
     if (!bytes) return FA_ERR_NULL;
     if (B < 1 || H < 1 || H_kv < 1 || H % H_kv != 0) return FA_ERR_SHAPE;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-    *bytes = 0;
+    unsigned int* err = nullptr;
+    int num_sms = 0, rc;
+    if ((rc = fa::device_error_word(&err, &num_sms)) != FA_OK) return rc;
+    const fa::Shape s = fa::shape_of(H, H_kv, d, num_sms);
+    if (s.bytes > 0x7fffffff) return FA_ERR_SHAPE;
+    *bytes = static_cast<int>(s.bytes);
     return FA_OK;
 }
 
@@ -145,6 +721,12 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     fa::DecodeFp8 p{};
     int num_sms = 0, rc;
     if ((rc = fa::device_error_word(&p.err, &num_sms)) != FA_OK) return rc;
+    const fa::Shape s = fa::shape_of(H, H_kv, d, num_sms);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    void* ws = nullptr;
+    if ((rc = fa::call_workspace(workspace, workspace_bytes, s.bytes, st, &ws)) != FA_OK) return rc;
+    p.part_lse = static_cast<float*>(ws);
+    p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + s.lse_bytes);
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.kp = static_cast<const uint8_t*>(k_pages);
     p.vp = static_cast<const uint8_t*>(v_pages);
@@ -157,15 +739,16 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     p.B = B;
     p.H = H;
     p.Hk = H_kv;
+    p.G = H / H_kv;
     p.num_pages = num_pages;
     p.table_len = table_len;
     p.max_pages = max_pages;
+    p.groups = s.groups;
+    p.group_heads = s.group_heads;
+    p.ranges = s.ranges;
     while ((1 << p.block_log2) < block) ++p.block_log2;
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (d == 64) fa::fa_decode_fp8_kernel<64><<<B * H, fa::kThreads, 0, st>>>(p);
-    else fa::fa_decode_fp8_kernel<128><<<B * H, fa::kThreads, 0, st>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    return d == 64 ? fa::launch<64>(p, s, st) : fa::launch<128>(p, s, st);
 }
 
 }  // extern "C"

@@ -284,6 +284,28 @@ def test_two_streams_and_two_graphs():
         assert torch.equal(w[0], x[0]) and torch.equal(w[1], x[1])
 
 
+def test_library_workspace_is_refused_in_a_capture_and_serves_outside_one():
+    c = Cache([9000, 300], 8, 2, 128, 64, "packed", seed=7)
+    want, wl = c.call()
+    table, o = c.table.cuda(), torch.empty_like(c.q)
+
+    def call():
+        return fa.lib().fa_decode_paged_fp8(
+            c.q.data_ptr(), c.kp.data_ptr(), c.vp.data_ptr(), c.ks.data_ptr(), c.vs.data_ptr(),
+            64, table.data_ptr(), len(table), 0, c.seq.data_ptr(), o.data_ptr(), None, 2, 8, 2,
+            c.kp.shape[0], 128, PS, c.scale, None, 0, torch.cuda.current_stream().cuda_stream)
+
+    assert call() == fa.FA_OK
+    _ok()
+    assert torch.equal(o, want)
+    got = []
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        x = torch.zeros(1, device="cuda")
+        got.append(call())
+        x += 1
+    assert got == [fa.FA_ERR_UNSUPPORTED]
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("table", ["packed", "rows"])
 def test_a_token_all_the_way(interleaved, table):
