@@ -5,6 +5,7 @@ stream; there is no fallback -- a missing library or a non-CUDA tensor is an
 error.
 """
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -589,21 +590,39 @@ _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "turns": 3, "yarn": 4}
 _FP8 = torch.float8_e4m3fn
 
 
-def _call(name: str, device, stream, *args):
-    """The library's `name` on `stream` (None: the device's current one), with
-    the tensors' device current for the call."""
+# The current stream of a GPU as a handle, without a Stream object around it
+# (1.2 us of a call that may take 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _call(name: str, dev: int, stream, *args):
+    """The library's `name` on `stream` (None: the current one of GPU `dev`, which
+    holds the tensors), with that GPU current for the call."""
     fn = getattr(lib(), name)
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the call's inputs on {device}")
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream.cuda_stream)
+        handle = _raw_stream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
+        raise ValueError(f"the stream is on {stream.device}, the call's inputs on GPU {dev}")
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, handle)
     if rc != FA_OK:
         raise FaError(rc, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes(name: str, dev: int, *sizes) -> int:
+    """The scratch that `name` gives for a call's sizes on GPU `dev`."""
+    n = ctypes.c_int(0)
+    fn = getattr(lib(), name)
+    with torch.cuda.device(dev):
+        _raise_if(fn(*sizes, ctypes.byref(n)), name)
+    return n.value
 
 
 def _empty(shape, dtype, device, stream):
@@ -615,57 +634,84 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _empty_like(t, stream):
+    # (of a tensor with gaps it makes a dense one, in the same order)
+    if stream is None:
+        return torch.empty_like(t)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _token_rows(t, name: str, device, shape=None) -> int:
+# These calls take a dozen tensors each, and a decode step's kernels are short:
+# a tensor that is as it should be is told by one expression, and what is wrong
+# with one that is not is found out afterwards.
+
+def _want(t, name: str, dtype, shape, dev: int):
+    """t: contiguous, of this type and shape, on GPU `dev`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.get_device() == dev and t.is_contiguous():
+        return
+    _check(t, name, dtype, len(shape))
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's inputs on GPU {dev}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _token_rows(t, name: str, dev=None, shape=None) -> int:
     """t: bf16 [tokens, heads, d] whose rows [heads, d] are contiguous, tokens
     any stride apart; returns that stride."""
-    if not isinstance(t, torch.Tensor) or t.device.type not in _DEVICE_TYPES:
+    if not isinstance(t, torch.Tensor) or (dev is None and t.device.type not in _DEVICE_TYPES):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or (shape is not None and t.shape != shape):
+    mine = t.shape
+    if len(mine) != 3 or (shape is not None and mine != shape):
         raise ValueError(f"{name} must have shape {shape or '[tokens, heads, d]'}, got "
-                         f"{tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's inputs on {device}")
-    tokens, heads, d = t.shape
+                         f"{tuple(mine)}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's inputs on GPU {dev}")
+    tokens, heads, d = mine
     st, sh, sd = t.stride()
+    if sd == 1 and sh == d and st >= heads * d and st % 8 == 0:
+        return st
     if (sd != 1 and d > 1) or (sh != d and heads > 1):
         raise ValueError(f"{name}: the [heads, d] part of a token must be contiguous")
     if tokens <= 1:
         return heads * d
-    if st < heads * d or st % 8 != 0:
-        raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart, without "
-                         f"overlap; got a stride of {st}")
-    return st
+    raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart, without "
+                     f"overlap; got a stride of {st}")
 
 
-def _norm_weights(q_weight, k_weight, d: int, device) -> int:
+def _norm_weights(q_weight, k_weight, d: int, dev: int) -> int:
     """The weights' type (FA_WEIGHT_*): [d] bf16 or fp32, one type, or None."""
-    dtype = torch.bfloat16
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            dtype = torch.float32 if w.dtype == torch.float32 else torch.bfloat16
-            _expect(w, n, dtype, (d,), device)
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise TypeError("q_weight and k_weight must have one type")
-    return int(dtype == torch.float32)
+    if q_weight is None and k_weight is None:
+        return 0
+    dtype = (k_weight if q_weight is None else q_weight).dtype
+    if dtype is not torch.float32:
+        dtype = torch.bfloat16
+    if q_weight is not None:
+        _want(q_weight, "q_weight", dtype, (d,), dev)
+    if k_weight is not None:
+        _want(k_weight, "k_weight", dtype, (d,), dev)
+    return int(dtype is torch.float32)
 
 
-def _rope(rope_cos, rope_sin, device):
+def _rope(rope_cos, rope_sin, dev: int):
     """(max_pos, rotary_dim) of the tables; (0, 0) without them."""
     if rope_cos is None and rope_sin is None:
         return 0, 0
     if rope_cos is None or rope_sin is None:
         raise ValueError("rope_cos and rope_sin come together")
-    _check(rope_cos, "rope_cos", torch.float32, 2)
-    _expect(rope_sin, "rope_sin", torch.float32, rope_cos.shape, device)
-    if rope_cos.device != device:
-        raise ValueError(f"rope_cos is on {rope_cos.device}, the call's inputs on {device}")
-    return rope_cos.shape[0], 2 * rope_cos.shape[1]
+    if not isinstance(rope_cos, torch.Tensor) or rope_cos.dim() != 2:
+        _check(rope_cos, "rope_cos", torch.float32, 2)
+    shape = rope_cos.shape
+    _want(rope_cos, "rope_cos", torch.float32, shape, dev)
+    _want(rope_sin, "rope_sin", torch.float32, shape, dev)
+    return shape[0], 2 * shape[1]
 
 
 def fa_rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling: str = "none",
@@ -683,56 +729,58 @@ def fa_rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling:
     if shape[0] < 1 or shape[1] < 1 or rotary_dim % 2 != 0:
         raise ValueError(f"max_pos must be positive and rotary_dim even, got {max_pos}, "
                          f"{rotary_dim}")
-    if device is None:
-        device = rope_cos.device if rope_cos is not None else \
-            torch.device("cuda", torch.cuda.current_device())
-    device = torch.device(device)
-    if device.type == "cuda" and device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
     if rope_cos is None:
+        if device is None:
+            device = rope_sin.device if rope_sin is not None else \
+                stream.device if stream is not None else "cuda"
         rope_cos = _empty(shape, torch.float32, device, stream)
     if rope_sin is None:
-        rope_sin = _empty(shape, torch.float32, device, stream)
-    _expect(rope_cos, "rope_cos", torch.float32, shape, device)
-    _expect(rope_sin, "rope_sin", torch.float32, shape, device)
-    _call("fa_rope_table", device, stream, rope_cos.data_ptr(), rope_sin.data_ptr(), shape[0],
-          int(rotary_dim), float(base), _SCALINGS[scaling], float(factor), int(original_len),
-          float(low), float(high), float(mscale))
+        rope_sin = _empty_like(rope_cos, stream)
+    dev = rope_cos.get_device()
+    _check(rope_cos, "rope_cos", torch.float32, 2)
+    _want(rope_cos, "rope_cos", torch.float32, shape, dev)
+    _want(rope_sin, "rope_sin", torch.float32, shape, dev)
+    _call("fa_rope_table", dev, stream, rope_cos.data_ptr(),
+          rope_sin.data_ptr(), shape[0], int(rotary_dim), float(base), _SCALINGS[scaling],
+          float(factor), int(original_len), float(low), float(high), float(mscale))
     return rope_cos, rope_sin
 
 
 def _qk_rows(q, k, positions):
-    """What the calls on queries and keys share: (layout, B, N, H, H_kv, d,
+    """What the calls on queries and keys share: (GPU, layout, B, N, H, H_kv, d,
     stride of q, stride of k), positions checked."""
     if isinstance(q, torch.Tensor) and q.dim() == 4:
         _check(q, "q", torch.bfloat16, 4)
+        dev = q.get_device()
         B, H, N, d = q.shape
         _check(k, "k", torch.bfloat16, 4)
         H_kv = k.shape[1]
-        _expect(k, "k", torch.bfloat16, (B, H_kv, N, d), q.device)
+        _want(k, "k", torch.bfloat16, (B, H_kv, N, d), dev)
         if positions is not None:
-            _expect(positions, "positions", torch.int32, (B, N), q.device)
-        return 1, B, N, H, H_kv, d, 0, 0
-    q_stride = _token_rows(q, "q", None)
-    k_stride = _token_rows(k, "k", q.device)
+            _want(positions, "positions", torch.int32, (B, N), dev)
+        return dev, 1, B, N, H, H_kv, d, 0, 0
+    q_stride = _token_rows(q, "q")
+    dev = q.get_device()
+    k_stride = _token_rows(k, "k", dev)
     N, H, d = q.shape
-    if k.shape[0] != N or k.shape[2] != d:
+    M, H_kv, dk = k.shape
+    if M != N or dk != d:
         raise ValueError(f"k must have q's tokens and d, got {tuple(k.shape)} and "
                          f"{tuple(q.shape)}")
     if positions is not None:
-        _expect(positions, "positions", torch.int32, (N,), q.device)
-    return 0, 1, N, H, k.shape[1], d, q_stride, k_stride
+        _want(positions, "positions", torch.int32, (N,), dev)
+    return dev, 0, 1, N, H, H_kv, d, q_stride, k_stride
 
 
 def _row_arg(t, name: str, like, layout: int, stream):
     """An output or a gradient of the same shape as `like` and its stride; made
     contiguous on the call's stream where it is None."""
     if t is None:
-        return _empty(like.shape, torch.bfloat16, like.device, stream), 0
+        return _empty_like(like, stream), 0
     if layout == 1:
-        _expect(t, name, torch.bfloat16, like.shape, like.device)
+        _want(t, name, torch.bfloat16, like.shape, like.get_device())
         return t, 0
-    return t, _token_rows(t, name, like.device, like.shape)
+    return t, _token_rows(t, name, like.get_device(), like.shape)
 
 
 def fa_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope_cos=None, rope_sin=None,
@@ -744,20 +792,17 @@ def fa_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope_cos=None, rope_sin=
     [tokens,H_kv,d] bf16, tokens any stride apart, positions [tokens] int32; or
     [B,H,N,d] and [B,H_kv,N,d] contiguous, positions [B,N].  No positions:
     token n is at position n.  The outputs may be the inputs."""
-    layout, B, N, H, H_kv, d, q_st, k_st = _qk_rows(q, k, positions)
-    device = q.device
-    wt = _norm_weights(q_weight, k_weight, d, device)
-    max_pos, rot = _rope(rope_cos, rope_sin, device)
+    dev, layout, B, N, H, H_kv, d, q_st, k_st = _qk_rows(q, k, positions)
+    wt = _norm_weights(q_weight, k_weight, d, dev)
+    max_pos, rot = _rope(rope_cos, rope_sin, dev)
     q_out, qo_st = _row_arg(q_out, "q_out", q, layout, stream)
     k_out, ko_st = _row_arg(k_out, "k_out", k, layout, stream)
-    if q.numel() == 0 or k.numel() == 0:
-        if B * N > 0:
-            raise ValueError("q and k need at least one head and value")
+    if B * N == 0:
         return q_out, k_out
-    _call("fa_qk_norm_rope", device, stream, q.data_ptr(), k.data_ptr(), q_out.data_ptr(),
-          k_out.data_ptr(), _ptr(q_weight), _ptr(k_weight), wt, _ptr(rope_cos), _ptr(rope_sin),
-          max_pos, rot, int(bool(interleaved)), _ptr(positions), layout, B, N, H, H_kv, d, q_st,
-          k_st, qo_st, ko_st, float(eps))
+    _call("fa_qk_norm_rope", dev, stream, q.data_ptr(), k.data_ptr(),
+          q_out.data_ptr(), k_out.data_ptr(), _ptr(q_weight), _ptr(k_weight), wt, _ptr(rope_cos),
+          _ptr(rope_sin), max_pos, rot, bool(interleaved), _ptr(positions), layout, B, N, H, H_kv,
+          d, q_st, k_st, qo_st, ko_st, eps)
     return q_out, k_out
 
 
@@ -776,10 +821,9 @@ def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope
     """Gradients of fa_qk_norm_rope: (dq, dk, dq_weight, dk_weight) from its
     inputs and its outputs' gradients; the weights' gradients are fp32 [d], None
     where there is no weight."""
-    layout, B, N, H, H_kv, d, q_st, k_st = _qk_rows(q, k, positions)
-    device = q.device
-    wt = _norm_weights(q_weight, k_weight, d, device)
-    max_pos, rot = _rope(rope_cos, rope_sin, device)
+    dev, layout, B, N, H, H_kv, d, q_st, k_st = _qk_rows(q, k, positions)
+    wt = _norm_weights(q_weight, k_weight, d, dev)
+    max_pos, rot = _rope(rope_cos, rope_sin, dev)
     for t, n in ((dq_out, "dq_out"), (dk_out, "dk_out")):
         if t is None:
             raise TypeError(f"{n} must be a CUDA tensor")
@@ -789,105 +833,109 @@ def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope
     dk, dk_st = _row_arg(dk, "dk", k, layout, stream)
     grads = []
     for w, g, n in ((q_weight, dq_weight, "dq_weight"), (k_weight, dk_weight, "dk_weight")):
-        if w is None and g is not None:
-            raise ValueError(f"{n} given without its weight")
-        if w is not None and g is None:
-            g = _empty((d,), torch.float32, device, stream)
         if g is not None:
-            _expect(g, n, torch.float32, (d,), device)
+            if w is None:
+                raise ValueError(f"{n} given without its weight")
+            _want(g, n, torch.float32, (d,), dev)
+        elif w is not None:
+            g = _empty((d,), torch.float32, q.device, stream)
         grads.append(g)
-    if q.numel() == 0 or k.numel() == 0:
-        if B * N > 0:
-            raise ValueError("q and k need at least one head and value")
+    if B * N == 0:
         with torch.cuda.stream(stream):
             for g in grads:
                 if g is not None:
                     g.zero_()
         return dq, dk, grads[0], grads[1]
-    ws = None
+    ws, n = None, 0
     if q_weight is not None or k_weight is not None:
-        n = _bytes_on(device, "fa_qk_norm_rope_bwd_workspace", B, N, H, H_kv, d)
-        ws = _empty((n,), torch.uint8, device, stream)
-    _call("fa_qk_norm_rope_bwd", device, stream, q.data_ptr(), k.data_ptr(), dq_out.data_ptr(),
-          dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(grads[0]), _ptr(grads[1]),
-          _ptr(q_weight), _ptr(k_weight), wt, _ptr(rope_cos), _ptr(rope_sin), max_pos, rot,
-          int(bool(interleaved)), _ptr(positions), layout, B, N, H, H_kv, d, q_st, k_st, gq_st,
-          gk_st, dq_st, dk_st, float(eps), _ptr(ws), 0 if ws is None else ws.numel())
+        n = _bytes("fa_qk_norm_rope_bwd_workspace", dev, B, N, H, H_kv, d)
+        ws = _empty((n,), torch.uint8, q.device, stream)
+    _call("fa_qk_norm_rope_bwd", dev, stream, q.data_ptr(), k.data_ptr(),
+          dq_out.data_ptr(), dk_out.data_ptr(), dq.data_ptr(), dk.data_ptr(), _ptr(grads[0]),
+          _ptr(grads[1]), _ptr(q_weight), _ptr(k_weight), wt, _ptr(rope_cos), _ptr(rope_sin),
+          max_pos, rot, bool(interleaved), _ptr(positions), layout, B, N, H, H_kv, d, q_st, k_st,
+          gq_st, gk_st, dq_st, dk_st, eps, _ptr(ws), n)
     return dq, dk, grads[0], grads[1]
 
 
-def _table(page_table, B: int, device):
+def _table(page_table, B: int, dev: int):
     """(entries, entries of a row) of a packed page table [n] (rows 0) or a
     block table [B, max_pages]."""
-    if isinstance(page_table, torch.Tensor) and page_table.dim() == 2:
-        _check(page_table, "page_table", torch.int32, 2)
-        if page_table.shape[0] != B:
-            raise ValueError("a block table must have one row per sequence")
-    else:
+    rows = isinstance(page_table, torch.Tensor) and page_table.dim() == 2
+    if not rows:
         _check(page_table, "page_table", torch.int32, 1)
-    if page_table.device != device:
-        raise ValueError(f"page_table is on {page_table.device}, the call's inputs on {device}")
-    return page_table.numel(), page_table.shape[1] if page_table.dim() == 2 else 0
+    shape = page_table.shape
+    if rows and shape[0] != B:
+        raise ValueError("a block table must have one row per sequence")
+    _want(page_table, "page_table", torch.int32, shape, dev)
+    return page_table.numel(), shape[1] if rows else 0
+
+
+def _pool(k_pages, v_pages, dtype, page_size: int, d: int, heads, dev: int):
+    """(pages, K/V heads) of a pool [P, heads, page_size, d], heads given or any."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        _check(k_pages, "k_pages", dtype, 4)
+    shape = k_pages.shape
+    P, H_kv = shape[0], shape[1]
+    _want(k_pages, "k_pages", dtype, shape, dev)
+    if v_pages.shape != shape or shape[2] != page_size or shape[3] != d or \
+            (heads is not None and H_kv != heads):
+        _pages(k_pages, v_pages, page_size, d, heads=heads)
+    _want(v_pages, "v_pages", dtype, shape, dev)
+    return P, H_kv
+
+
+def _scale_block(k_scales, v_scales, P: int, H_kv: int, page_size: int, dev: int) -> int:
+    """Tokens that share a scale: scales [P, H_kv, page_size / block] fp32."""
+    _check(k_scales, "k_scales", torch.float32, 3)
+    shape = k_scales.shape
+    n = shape[2]
+    if shape[0] != P or shape[1] != H_kv or n < 1 or page_size % n != 0:
+        raise ValueError(f"scales must be [{P}, {H_kv}, {page_size} / block], got "
+                         f"{tuple(shape)}")
+    _want(k_scales, "k_scales", torch.float32, shape, dev)
+    _want(v_scales, "v_scales", torch.float32, shape, dev)
+    return page_size // n
 
 
 def _append(name, q_new, k_new, v_new, cu_new, k_pages, v_pages, scales, page_table, seq_lens,
             rope_cos, rope_sin, q_weight, k_weight, eps, interleaved, page_size, q_out, stream):
     """Checks and call of both appends; `scales`: (k_scales, v_scales) or ()."""
-    k_st = _token_rows(k_new, "k_new", None)
-    device = k_new.device
-    v_st = _token_rows(v_new, "v_new", device, k_new.shape)
-    total, H_kv, d = k_new.shape
+    k_st = _token_rows(k_new, "k_new")
+    dev = k_new.get_device()
+    total, H_kv, d = shape = k_new.shape
+    v_st = _token_rows(v_new, "v_new", dev, shape)
     H, q_st = 0, 0
     if q_new is not None:
-        q_st = _token_rows(q_new, "q_new", device)
-        H = q_new.shape[1]
-        if q_new.shape != (total, H, d):
-            raise ValueError(f"q_new must have k_new's tokens and d, got {tuple(q_new.shape)}")
+        q_st = _token_rows(q_new, "q_new", dev)
+        q_shape = q_new.shape
+        H = q_shape[1]
+        if q_shape[0] != total or q_shape[2] != d:
+            raise ValueError(f"q_new must have k_new's tokens and d, got {tuple(q_shape)}")
         if q_out is None:
-            q_out = _empty((total, H, d), torch.bfloat16, device, stream)
-        _expect(q_out, "q_out", torch.bfloat16, (total, H, d), device)
+            q_out = _empty_like(q_new, stream)
+        else:
+            _want(q_out, "q_out", torch.bfloat16, q_shape, dev)
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q_new")
-    dtype = _FP8 if scales else torch.bfloat16
-    _check(k_pages, "k_pages", dtype, 4)
-    _check(v_pages, "v_pages", dtype, 4)
-    _pages(k_pages, v_pages, page_size, d, heads=H_kv)
+    P, _ = _pool(k_pages, v_pages, _FP8 if scales else torch.bfloat16, page_size, d, H_kv, dev)
     _check(cu_new, "cu_new", torch.int32, 1)
     B = cu_new.numel() - 1
-    _check(seq_lens, "seq_lens", torch.int32, 1)
-    if seq_lens.numel() != B:
-        raise ValueError("seq_lens must hold one length per sequence of cu_new")
-    _same_device(device, cu_new=cu_new, k_pages=k_pages, v_pages=v_pages, seq_lens=seq_lens)
-    table_len, max_pages = _table(page_table, B, device)
-    block = ()
-    if scales:
-        block = (_scale_block(scales, k_pages, device),)
-    wt = _norm_weights(q_weight, k_weight, d, device)
-    max_pos, rot = _rope(rope_cos, rope_sin, device)
+    _want(cu_new, "cu_new", torch.int32, (B + 1,), dev)
+    _want(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    table_len, max_pages = _table(page_table, B, dev)
+    block = (_scale_block(*scales, P, H_kv, page_size, dev),) if scales else ()
+    wt = _norm_weights(q_weight, k_weight, d, dev)
+    max_pos, rot = _rope(rope_cos, rope_sin, dev)
     if total == 0:
         return q_out
-    _call(name, device, stream, _ptr(q_new), k_new.data_ptr(), v_new.data_ptr(),
+    _call(name, dev, stream, _ptr(q_new), k_new.data_ptr(), v_new.data_ptr(),
           cu_new.data_ptr(), _ptr(q_out), k_pages.data_ptr(), v_pages.data_ptr(),
-          *(s.data_ptr() for s in scales), *block, page_table.data_ptr() or seq_lens.data_ptr(),
+          *[s.data_ptr() for s in scales], *block, page_table.data_ptr() or seq_lens.data_ptr(),
           table_len, max_pages, seq_lens.data_ptr(), _ptr(q_weight), _ptr(k_weight), wt,
-          _ptr(rope_cos), _ptr(rope_sin), max_pos, rot, int(bool(interleaved)), B, H, H_kv,
-          total, k_pages.shape[0], d, int(page_size), q_st, k_st, v_st, float(eps))
+          _ptr(rope_cos), _ptr(rope_sin), max_pos, rot, bool(interleaved), B, H, H_kv, total, P,
+          d, page_size, q_st, k_st, v_st, eps)
     return q_out
-
-
-def _scale_block(scales, pages, device) -> int:
-    """Tokens that share a scale: scales [P, H_kv, page_size / block] fp32."""
-    for s, n in zip(scales, ("k_scales", "v_scales")):
-        _check(s, n, torch.float32, 3)
-        if s.device != device:
-            raise ValueError(f"{n} is on {s.device}, the call's inputs on {device}")
-    P, heads, page_size = pages.shape[:3]
-    n = scales[0].shape[2]
-    if scales[1].shape != scales[0].shape or scales[0].shape[:2] != (P, heads) or n < 1 or \
-            page_size % n != 0:
-        raise ValueError(f"scales must be [{P}, {heads}, {page_size} / block], got "
-                         f"{tuple(scales[0].shape)} and {tuple(scales[1].shape)}")
-    return page_size // n
 
 
 def fa_append_paged_rope(q_new, k_new, v_new, cu_new, k_pages, v_pages, page_table, seq_lens,
@@ -932,47 +980,30 @@ def fa_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, page_table, seq
     packed [n] or a block table [B, max_pages] -> o [B,H,d] bf16; `lse` [B,H]
     fp32 is filled where it is given."""
     _check(q, "q", torch.bfloat16, 3)
-    _check(k_pages, "k_pages", _FP8, 4)
-    _check(v_pages, "v_pages", _FP8, 4)
-    _check(seq_lens, "seq_lens", torch.int32, 1)
-    B, H, d = q.shape
-    device = q.device
-    _pages(k_pages, v_pages, page_size, d)
-    H_kv = k_pages.shape[1]
+    dev = q.get_device()
+    B, H, d = shape = q.shape
+    P, H_kv = _pool(k_pages, v_pages, _FP8, page_size, d, None, dev)
     if H_kv == 0 or H % H_kv != 0:
         raise ValueError(f"H ({H}) must be a multiple of the cache's K/V heads ({H_kv})")
-    if seq_lens.numel() != B:
-        raise ValueError(f"seq_lens must hold one length per sequence ({B})")
-    _same_device(device, k_pages=k_pages, v_pages=v_pages, seq_lens=seq_lens)
-    block = _scale_block((k_scales, v_scales), k_pages, device)
-    table_len, max_pages = _table(page_table, B, device)
+    _want(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    block = _scale_block(k_scales, v_scales, P, H_kv, page_size, dev)
+    table_len, max_pages = _table(page_table, B, dev)
     if o is None:
-        o = _empty(q.shape, torch.bfloat16, device, stream)
-    _expect(o, "o", torch.bfloat16, q.shape, device)
+        o = _empty_like(q, stream)
+    else:
+        _want(o, "o", torch.bfloat16, shape, dev)
     if lse is not None:
-        _expect(lse, "lse", torch.float32, (B, H), device)
-    if q.numel() == 0:
+        _want(lse, "lse", torch.float32, (B, H), dev)
+    if B == 0:
         return o
-    n = _bytes_on(device, "fa_decode_paged_fp8_workspace", B, H, H_kv, d)
-    ws = _empty((n,), torch.uint8, device, stream) if n else None
-    _call("fa_decode_paged_fp8", device, stream, q.data_ptr(), k_pages.data_ptr(),
+    n = _bytes("fa_decode_paged_fp8_workspace", dev, B, H, H_kv, d)
+    ws = _empty((n,), torch.uint8, q.device, stream)
+    _call("fa_decode_paged_fp8", dev, stream, q.data_ptr(), k_pages.data_ptr(),
           v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block,
           page_table.data_ptr() or seq_lens.data_ptr(), table_len, max_pages,
-          seq_lens.data_ptr(), o.data_ptr(), _ptr(lse), B, H, H_kv, k_pages.shape[0], d,
-          int(page_size), d ** -0.5 if scale is None else float(scale), _ptr(ws), n)
+          seq_lens.data_ptr(), o.data_ptr(), _ptr(lse), B, H, H_kv, P, d, page_size,
+          d ** -0.5 if scale is None else scale, ws.data_ptr(), n)
     return o
-
-
-def _bytes_on(device, name: str, *sizes) -> int:
-    """A call's scratch on `device` (what `name` gives there)."""
-    fn, n = getattr(lib(), name), ctypes.c_int(0)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*sizes, ctypes.byref(n))
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*sizes, ctypes.byref(n))
-    _raise_if(rc, name)
-    return n.value
 
 
 def fa_get_device_error(stream=None) -> int:
