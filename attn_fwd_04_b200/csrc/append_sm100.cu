@@ -144,13 +144,14 @@ __global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const Append p
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     __shared__ Shared sh;
     const int r = blockIdx.x;
-    const int lane = threadIdx.x & 31, chunk = threadIdx.x % LPR, my = threadIdx.x / LPR;
+    const int my = threadIdx.x / LPR;
     const Seq s = find_row(p, r, sh);
     if (!s.found) return;
     const int pos = s.bad ? 0 : s.len - s.n + (r - s.row0);
     const int page = s.bad ? -1 : page_at(p, s, pos);
+    const Lane<D, INTER> lane(p.t.half);
     Rotation<D, INTER> rot;
-    rot.load(p.t, pos, lane, 1.f);
+    rot.load(p.t, pos, lane);
     __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(p.kp);
     __nv_bfloat16* vp = static_cast<__nv_bfloat16*>(p.vp);
     const int rows = p.H + 2 * p.Hk;
@@ -160,9 +161,7 @@ __global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const Append p
         const int h = is_q ? i : is_k ? i - p.H : min(i - p.H - p.Hk, p.Hk - 1);
         const __nv_bfloat16* x = is_q ? p.q + r * p.sq : is_k ? p.k + r * p.sk : p.v + r * p.sv;
         uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live)
-            raw = __ldcs(
-                reinterpret_cast<const uint4*>(x + static_cast<int64_t>(h) * D + chunk * 8));
+        if (live) raw = lane.load(x + static_cast<int64_t>(h) * D);
         float y[8];
         unpack8(raw, y);
         if (p.wq.w || p.wk.w) {
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const Append p
             const NormWeight nw = is_q ? p.wq : p.wk;
             if (nw.w && (is_q || is_k)) {
                 float w[8];
-                load_weight8(nw, chunk, w);
+                lane.weights(nw, w);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) y[j] *= rs * w[j];
             }
@@ -178,13 +177,12 @@ __global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const Append p
         rot.apply(y);
         if (!live) continue;
         if (is_q) {
-            *reinterpret_cast<uint4*>(p.qo + (static_cast<int64_t>(r) * p.H + h) * D + chunk * 8) =
-                s.bad ? make_uint4(0, 0, 0, 0) : pack8(y);
+            lane.store(p.qo + (static_cast<int64_t>(r) * p.H + h) * D,
+                       s.bad ? make_uint4(0, 0, 0, 0) : pack8(y));
         } else if (page >= 0) {
-            const int64_t at =
-                ((static_cast<int64_t>(page) * p.Hk + h) * kPage + pos % kPage) * D + chunk * 8;
-            if (is_k) *reinterpret_cast<uint4*>(kp + at) = pack8(y);
-            else *reinterpret_cast<uint4*>(vp + at) = raw;  // values as they are
+            const int64_t at = ((static_cast<int64_t>(page) * p.Hk + h) * kPage + pos % kPage) * D;
+            if (is_k) lane.store(kp + at, pack8(y));
+            else lane.store(vp + at, raw);  // values as they are
         }
     }
 }
@@ -322,7 +320,8 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append p)
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     __shared__ Shared sh;
     __shared__ float red[kWarps];
-    const int lane = threadIdx.x & 31, chunk = threadIdx.x % LPR, my = threadIdx.x / LPR;
+    const int my = threadIdx.x / LPR;
+    const Lane<D, INTER> lane(p.t.half);
     const int kv_ctas = p.units * 2 * p.Hk;
     if (static_cast<int>(blockIdx.x) >= kv_ctas) {
         // query rows: one token's heads over a CTA's slots
@@ -331,20 +330,20 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append p)
         if (!s.found) return;
         const int pos = s.bad ? 0 : s.len - s.n + (r - s.row0);
         Rotation<D, INTER> rot;
-        rot.load(p.t, pos, lane, 1.f);
+        rot.load(p.t, pos, lane);
+        float w[8];
+        if (p.wq.w) lane.weights(p.wq, w);
         for (int h = my; h - my < p.H; h += SL) {
             const bool live = h < p.H;
             uint4 raw = make_uint4(0, 0, 0, 0);
-            if (live)
-                raw = __ldcs(reinterpret_cast<const uint4*>(
-                    p.q + r * p.sq + static_cast<int64_t>(h) * D + chunk * 8));
+            if (live) raw = lane.load(p.q + r * p.sq + static_cast<int64_t>(h) * D);
             float y[8];
             unpack8(raw, y);
-            norm_row<D>(y, p.wq, chunk, p.eps);
+            if (p.wq.w) norm_row<D>(y, w, p.eps);
             rot.apply(y);
             if (live)
-                *reinterpret_cast<uint4*>(p.qo + (static_cast<int64_t>(r) * p.H + h) * D +
-                                          chunk * 8) = s.bad ? make_uint4(0, 0, 0, 0) : pack8(y);
+                lane.store(p.qo + (static_cast<int64_t>(r) * p.H + h) * D,
+                           s.bad ? make_uint4(0, 0, 0, 0) : pack8(y));
         }
         return;
     }
@@ -359,17 +358,18 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append p)
     const int first = max(lo, start), last = min(lo + (1 << lg), s.len);
     const int page = page_at(p, s, lo);
     if (page < 0) return;
-    const __nv_bfloat16* x =
-        (is_k ? p.k : p.v) + static_cast<int64_t>(h) * D + chunk * 8;
+    const __nv_bfloat16* x = (is_k ? p.k : p.v) + static_cast<int64_t>(h) * D;
     const int64_t sx = is_k ? p.sk : p.sv;
-    const NormWeight nw = is_k ? p.wk : NormWeight{nullptr, 0};
+    const bool norms = is_k && p.wk.w;
+    float w[8];
+    if (norms) lane.weights(p.wk, w);
     // row `pos` of the new tokens, normed and rotated
     auto row = [&](int pos, float (&y)[8]) {
-        unpack8(__ldg(reinterpret_cast<const uint4*>(x + (s.row0 + (pos - start)) * sx)), y);
-        norm_row<D>(y, nw, chunk, p.eps);
+        unpack8(lane.load(x + (s.row0 + (pos - start)) * sx), y);
+        if (norms) norm_row<D>(y, w, p.eps);
         if (is_k) {
             Rotation<D, INTER> rot;
-            rot.load(p.t, pos, lane, 1.f);
+            rot.load(p.t, pos, lane);
             rot.apply(y);
         }
     };
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append p)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (lane == 0) red[threadIdx.x >> 5] = amax;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
     const int64_t slice = static_cast<int64_t>(page) * p.Hk + h;
     float* scale = (is_k ? p.ks : p.vs) + slice * (kPage >> lg) + ((lo % kPage) >> lg);
     const float was = first > lo ? *scale : 0.f;
@@ -395,25 +395,24 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append p)
     const int e = scale_exponent(amax);
     const float now = fmaxf(was, ldexpf(1.f, e));
     uint8_t* dst = static_cast<uint8_t*>(is_k ? p.kp : p.vp) +
-                   (slice * kPage + lo % kPage) * D + chunk * 8;
+                   (slice * kPage + lo % kPage) * D;
     if (threadIdx.x == 0) *scale = now;
     if (first > lo && now != was) {  // earlier tokens under the larger scale
         const float ratio = was / now;  // now is a power of two
         for (int i = my; i < first - lo; i += SL) {
             float y[8];
-            uint2* c = reinterpret_cast<uint2*>(dst + static_cast<int64_t>(i) * D);
-            decode8(*c, y);
+            uint8_t* c = dst + static_cast<int64_t>(i) * D;
+            decode8(lane.load(c), y);
 #pragma unroll
             for (int j = 0; j < 8; ++j) y[j] *= ratio;
-            *c = encode8(y);
+            lane.store(c, encode8(y));
         }
     }
     for (int i = first + my; i - my < last; i += SL) {
         float y[8];
         row(min(i, last - 1), y);
         divide8(y, now);
-        if (i < last)
-            *reinterpret_cast<uint2*>(dst + static_cast<int64_t>(i - lo) * D) = encode8(y);
+        if (i < last) lane.store(dst + static_cast<int64_t>(i - lo) * D, encode8(y));
     }
 }
 

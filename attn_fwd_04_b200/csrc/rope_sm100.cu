@@ -83,70 +83,93 @@ struct Rows {
     }
 };
 
+// One of the two tensors of a call: queries or keys.
+struct Side {
+    const __nv_bfloat16* x;  // the rows to norm
+    const __nv_bfloat16* g;  // backward: gradients of the outputs
+    __nv_bfloat16* y;        // outputs, or gradients of the rows
+    Rows rx, rg, ry;
+    NormWeight w;
+    int heads, groups;  // groups of U heads
+    uint32_t slots;     // tokens * groups
+    int ctas;           // CTAs of the grid that take this side
+};
+
 struct NormRope {
-    const __nv_bfloat16 *q, *k;    // the rows to norm
-    const __nv_bfloat16 *gq, *gk;  // backward: gradients of the outputs
-    __nv_bfloat16 *qo, *ko;        // outputs, or gradients of the rows
-    Rows rq, rk, rgq, rgk, rqo, rko;
-    NormWeight wq, wk;
+    Side q, k;
     RopeTable t;
     const int32_t* positions;
-    int N, H, Hk;
-    int gq_groups, groups;  // groups of U heads of one token: of queries, of both
-    int64_t slots;          // tokens * groups
+    int N;
+    bool heads_first;
     float eps;
-    float* part;  // backward: [grid, 2, D] partial weight gradients
+    float* part;  // backward: [CTAs, D] partial weight gradients
     unsigned int* err;
 };
 
-// D / 8 lanes take U heads of one token, so that the token's table entries are
-// read once for U rows and U loads are in flight.
-template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const NormRope p) {
-    constexpr int LPR = D / 8;
-    const int lane = threadIdx.x & 31, chunk = threadIdx.x % LPR;
-    const int64_t slot = static_cast<int64_t>(blockIdx.x) * (kThreads / LPR) + threadIdx.x / LPR;
-    const bool live = slot < p.slots;
-    const int64_t sl = live ? slot : p.slots - 1;
-    const int64_t token = sl / p.groups;
-    const int group = static_cast<int>(sl - token * p.groups);
-    const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<int64_t>(b) * p.N);
-    const bool is_q = group < p.gq_groups;
-    const int heads = is_q ? p.H : p.Hk;
-    const int h0 = (is_q ? group : group - p.gq_groups) * U;
-    const __nv_bfloat16* x = is_q ? p.q : p.k;
-    const Rows& rx = is_q ? p.rq : p.rk;
-    uint4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-        raw[u] = __ldcs(reinterpret_cast<const uint4*>(
-            x + rx.at(b, n, min(h0 + u, heads - 1)) + chunk * 8));
-    int pos = p.positions ? __ldg(p.positions + token) : n;
-    const bool bad = p.t.half > 0 && (pos < 0 || pos >= p.t.max_pos);
-    if (bad) pos = 0;
-    if (bad && live && chunk == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
-    Rotation<D, INTER> rot;
-    rot.load(p.t, pos, lane, 1.f);
-    const NormWeight nw = is_q ? p.wq : p.wk;
-    const bool norms = p.wq.w || p.wk.w;
-    float w[8];
-    if (nw.w) load_weight8(nw, chunk, w);
-    __nv_bfloat16* y = is_q ? p.qo : p.ko;
-    const Rows& ry = is_q ? p.rqo : p.rko;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        float v[8];
-        unpack8(raw[u], v);
-        // the lanes of a warp may hold rows of q and of k: all take the sum
-        const float r = norms ? row_rstd<D>(v, p.eps) : 1.f;
-        if (nw.w) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= r * w[j];
+// A slot is U heads of one token, taken by D / 8 lanes: the token's table
+// entries are read once for U rows, and U loads are in flight.  Slots next to
+// each other are next to each other in memory: the groups of heads of a token
+// where tokens come first, the tokens of a group where heads do.
+struct Slot {
+    int b, n, h0;
+    __device__ __forceinline__ Slot(const NormRope& p, const Side& s, uint32_t i, int U) {
+        if (p.heads_first) {
+            const uint32_t outer = i / static_cast<uint32_t>(p.N);
+            n = static_cast<int>(i - outer * p.N);
+            b = static_cast<int>(outer / static_cast<uint32_t>(s.groups));
+            h0 = static_cast<int>(outer - static_cast<uint32_t>(b) * s.groups) * U;
+        } else {
+            b = 0;
+            n = static_cast<int>(i / static_cast<uint32_t>(s.groups));
+            h0 = static_cast<int>(i - static_cast<uint32_t>(n) * s.groups) * U;
         }
-        rot.apply(v);
-        if (live && h0 + u < heads) {
-            const uint4 out = bad ? make_uint4(0, 0, 0, 0) : pack8(v);
-            *reinterpret_cast<uint4*>(y + ry.at(b, n, h0 + u) + chunk * 8) = out;
+    }
+    // The token's position in the tables; out of them: 0, and bad.
+    __device__ __forceinline__ int position(const NormRope& p, bool& bad) const {
+        const int pos = p.positions ? __ldg(p.positions + static_cast<int64_t>(b) * p.N + n) : n;
+        bad = p.t.half > 0 && (pos < 0 || pos >= p.t.max_pos);
+        return bad ? 0 : pos;
+    }
+};
+
+// The grid's first CTAs take the queries, the others the keys, each in equal
+// strides over its slots: a CTA's weights stay in registers.
+template <int D, bool INTER, int U>
+__global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const __grid_constant__ NormRope p) {
+    constexpr int LPR = D / 8, SL = kThreads / LPR;
+    const Lane<D, INTER> lane(p.t.half);
+    const bool is_q = static_cast<int>(blockIdx.x) < p.q.ctas;
+    const Side& s = is_q ? p.q : p.k;
+    const uint32_t stride = static_cast<uint32_t>(s.ctas) * SL;
+    const bool norms = s.w.w != nullptr;
+    float w[8];
+    if (norms) lane.weights(s.w, w);
+    // all lanes of a warp stay together: the last slot stands in for those behind it
+    for (uint32_t base = (blockIdx.x - (is_q ? 0 : p.q.ctas)) * SL; base < s.slots;
+         base += stride) {
+        const uint32_t i = base + threadIdx.x / LPR;
+        const bool live = i < s.slots;
+        const Slot at(p, s, live ? i : s.slots - 1, U);
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (at.h0 + u < s.heads) raw[u] = lane.load(s.x + s.rx.at(at.b, at.n, at.h0 + u));
+        }
+        bool bad;
+        const int pos = at.position(p, bad);
+        if (bad && live && lane.chunk == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
+        Rotation<D, INTER> rot;
+        rot.load(p.t, pos, lane);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float v[8];
+            unpack8(raw[u], v);
+            if (norms) norm_row<D>(v, w, p.eps);
+            rot.apply(v);
+            if (live && at.h0 + u < s.heads)
+                lane.store(s.y + s.ry.at(at.b, at.n, at.h0 + u),
+                           bad ? make_uint4(0, 0, 0, 0) : pack8(v));
         }
     }
 }
@@ -157,94 +180,78 @@ __global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const NormRope p
 // thread sums dw over its rows in registers, the CTA over its threads in
 // shared memory, and a second kernel over the CTAs in fp64: a fixed order.
 template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads) fa_norm_rope_bwd_kernel(const NormRope p) {
+__global__ void __launch_bounds__(kThreads)
+    fa_norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     __shared__ float red[SL][D];
-    const int lane = threadIdx.x & 31, chunk = threadIdx.x % LPR, my = threadIdx.x / LPR;
-    const bool norms = p.wq.w || p.wk.w;
-    float accq[8], acck[8];
+    const Lane<D, INTER> lane(p.t.half);
+    const bool is_q = static_cast<int>(blockIdx.x) < p.q.ctas;
+    const Side& s = is_q ? p.q : p.k;
+    const uint32_t stride = static_cast<uint32_t>(s.ctas) * SL;
+    const bool norms = s.w.w != nullptr;
+    float w[8], acc[8];
+    if (norms) lane.weights(s.w, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) accq[j] = acck[j] = 0.f;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * SL; base < p.slots;
-         base += static_cast<int64_t>(gridDim.x) * SL) {
-        const int64_t slot = base + my;
-        const bool live = slot < p.slots;
-        const int64_t sl = live ? slot : p.slots - 1;
-        const int64_t token = sl / p.groups;
-        const int group = static_cast<int>(sl - token * p.groups);
-        const int b = static_cast<int>(token / p.N), n = static_cast<int>(token - static_cast<int64_t>(b) * p.N);
-        const bool is_q = group < p.gq_groups;
-        const int heads = is_q ? p.H : p.Hk;
-        const int h0 = (is_q ? group : group - p.gq_groups) * U;
-        const NormWeight nw = is_q ? p.wq : p.wk;
-        const __nv_bfloat16* x = is_q ? p.q : p.k;
-        const __nv_bfloat16* g = is_q ? p.gq : p.gk;
-        const Rows& rx = is_q ? p.rq : p.rk;
-        const Rows& rg = is_q ? p.rgq : p.rgk;
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    for (uint32_t base = (blockIdx.x - (is_q ? 0 : p.q.ctas)) * SL; base < s.slots;
+         base += stride) {
+        const uint32_t i = base + threadIdx.x / LPR;
+        const bool live = i < s.slots;
+        const Slot at(p, s, live ? i : s.slots - 1, U);
         uint4 gr[U], xr[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int h = min(h0 + u, heads - 1);
-            gr[u] = __ldcs(reinterpret_cast<const uint4*>(g + rg.at(b, n, h) + chunk * 8));
-            xr[u] = make_uint4(0, 0, 0, 0);
-            if (nw.w)
-                xr[u] = __ldcs(reinterpret_cast<const uint4*>(x + rx.at(b, n, h) + chunk * 8));
+            gr[u] = xr[u] = make_uint4(0, 0, 0, 0);
+            if (at.h0 + u < s.heads) {
+                gr[u] = lane.load(s.g + s.rg.at(at.b, at.n, at.h0 + u));
+                if (norms) xr[u] = lane.load(s.x + s.rx.at(at.b, at.n, at.h0 + u));
+            }
         }
-        int pos = p.positions ? __ldg(p.positions + token) : n;
-        const bool bad = p.t.half > 0 && (pos < 0 || pos >= p.t.max_pos);
-        if (bad) pos = 0;
-        if (bad && live && chunk == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
+        bool bad;
+        const int pos = at.position(p, bad);
+        if (bad && live && lane.chunk == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
         Rotation<D, INTER> rot;
-        rot.load(p.t, pos, lane, -1.f);
-        float w[8];
-        if (nw.w) load_weight8(nw, chunk, w);
-        __nv_bfloat16* y = is_q ? p.qo : p.ko;
-        const Rows& ry = is_q ? p.rqo : p.rko;
+        rot.template load<true>(p.t, pos, lane);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float gv[8], xv[8];
+            float gv[8];
             unpack8(gr[u], gv);
-            unpack8(xr[u], xv);
             rot.apply(gv);
-            const bool mine = live && h0 + u < heads;
-            const float r = norms ? row_rstd<D>(xv, p.eps) : 1.f;
-            float dot = 0.f;
-            if (nw.w) {
+            const bool mine = live && at.h0 + u < s.heads;
+            if (norms) {
+                float xv[8];
+                unpack8(xr[u], xv);
+                const float r = row_rstd<D>(xv, p.eps);
+                float dot = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float hat = xv[j] * r;
-                    if (mine && !bad) {
-                        if (is_q) accq[j] = fmaf(gv[j], hat, accq[j]);
-                        else acck[j] = fmaf(gv[j], hat, acck[j]);
-                    }
-                    xv[j] = hat;
+                    xv[j] *= r;
+                    if (mine && !bad) acc[j] = fmaf(gv[j], xv[j], acc[j]);
                     gv[j] *= w[j];
-                    dot = fmaf(gv[j], hat, dot);
+                    dot = fmaf(gv[j], xv[j], dot);
                 }
-            }
-            if (norms) dot = row_sum<D>(dot) * (1.f / D);
-            if (nw.w) {
+                dot = row_sum<D>(dot) * (1.f / D);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) gv[j] = r * (gv[j] - xv[j] * dot);
             }
-            if (mine) {
-                const uint4 out = bad ? make_uint4(0, 0, 0, 0) : pack8(gv);
-                *reinterpret_cast<uint4*>(y + ry.at(b, n, h0 + u) + chunk * 8) = out;
-            }
+            if (mine)
+                lane.store(s.y + s.ry.at(at.b, at.n, at.h0 + u),
+                           bad ? make_uint4(0, 0, 0, 0) : pack8(gv));
         }
     }
-    if (p.part == nullptr) return;
+    if (!norms) return;  // the whole CTA
+    const int my = threadIdx.x / LPR;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    for (int j = 0; j < 4; ++j) {
+        red[my][lane.lo + j] = acc[j];
+        red[my][lane.hi + j] = acc[4 + j];
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) red[my][chunk * 8 + j] = which ? acck[j] : accq[j];
-        __syncthreads();
-        if (threadIdx.x < D) {
-            float s = 0.f;
-            for (int i = 0; i < SL; ++i) s += red[i][threadIdx.x];
-            p.part[(static_cast<int64_t>(blockIdx.x) * 2 + which) * D + threadIdx.x] = s;
-        }
-        __syncthreads();
+        for (int i = 0; i < SL; ++i) sum += red[i][threadIdx.x];
+        p.part[static_cast<int64_t>(blockIdx.x) * D + threadIdx.x] = sum;
     }
 }
 
@@ -252,18 +259,21 @@ __global__ void __launch_bounds__(kThreads) fa_norm_rope_bwd_kernel(const NormRo
 constexpr int kSumRows = 8;
 template <int D>
 __global__ void __launch_bounds__(D* kSumRows)
-    fa_norm_rope_dw_kernel(const float* __restrict__ part, int ctas, float* __restrict__ dwq,
-                           float* __restrict__ dwk) {
+    fa_norm_rope_dw_kernel(const float* __restrict__ part, int q_ctas, int ctas,
+                           float* __restrict__ dwq, float* __restrict__ dwk) {
     __shared__ double red[kSumRows][D];
     const int col = threadIdx.x % D, row = threadIdx.x / D;
     float* dst = blockIdx.x == 0 ? dwq : dwk;
+    if (dst == nullptr) return;
+    const int end = blockIdx.x == 0 ? q_ctas : ctas;
     double s = 0.0;
-    if (dst)
-        for (int i = row; i < ctas; i += kSumRows)
-            s += part[(static_cast<int64_t>(i) * 2 + blockIdx.x) * D + col];
+#pragma unroll 8
+    for (int i = (blockIdx.x == 0 ? 0 : q_ctas) + row; i < end; i += kSumRows)
+        s += part[static_cast<int64_t>(i) * D + col];
     red[row][col] = s;
     __syncthreads();
-    if (row == 0 && dst) {
+    if (row == 0) {
+#pragma unroll
         for (int i = 1; i < kSumRows; ++i) s += red[i][col];
         dst[col] = static_cast<float>(s);
     }
@@ -273,7 +283,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 constexpr int kFwdHeads = 4;  // heads a slot takes
 constexpr int kBwdHeads = 2;
-constexpr int kBwdCtas = 4;  // CTAs per SM of the backward kernel's grid
+constexpr int kFwdCtas = 32;  // CTAs per SM of the grids, at most
+constexpr int kBwdCtas = 4;
 
 // The rows of a tensor with `heads` heads: packed tokens `stride` apart (0:
 // back to back), or [B, heads, N, d].
@@ -307,61 +318,69 @@ int fill(NormRope& p, const void* q, const void* k, void* qo, void* ko, const vo
     if (weight_type != FA_WEIGHT_BF16 && weight_type != FA_WEIGHT_FP32) return FA_ERR_UNSUPPORTED;
     if (!std::isfinite(eps) || eps < 0.f) return FA_ERR_SHAPE;
     if (rotary_dim > 0 && (max_pos < 1 || (!positions && max_pos < N))) return FA_ERR_SHAPE;
-    // one slot of a CTA takes at least one row; the grid's x has 2^31 - 1 CTAs
-    const int64_t tokens = static_cast<int64_t>(B) * N;
-    if (tokens > (int64_t{1} << 34) / (static_cast<int64_t>(H) + H_kv)) return FA_ERR_SHAPE;
+    // rows are counted in 32 bits: 2^31 of them would fill 256 GB and more
+    if (static_cast<int64_t>(B) * N > 0x7fffffff / (static_cast<int64_t>(H) + H_kv))
+        return FA_ERR_SHAPE;
     int rc;
-    if ((rc = rows_of(layout, H, N, d, q_stride, &p.rq)) != FA_OK) return rc;
-    if ((rc = rows_of(layout, H_kv, N, d, k_stride, &p.rk)) != FA_OK) return rc;
-    if ((rc = rows_of(layout, H, N, d, qo_stride, &p.rqo)) != FA_OK) return rc;
-    if ((rc = rows_of(layout, H_kv, N, d, ko_stride, &p.rko)) != FA_OK) return rc;
+    if ((rc = rows_of(layout, H, N, d, q_stride, &p.q.rx)) != FA_OK) return rc;
+    if ((rc = rows_of(layout, H_kv, N, d, k_stride, &p.k.rx)) != FA_OK) return rc;
+    if ((rc = rows_of(layout, H, N, d, qo_stride, &p.q.ry)) != FA_OK) return rc;
+    if ((rc = rows_of(layout, H_kv, N, d, ko_stride, &p.k.ry)) != FA_OK) return rc;
     if (!aligned16(q) || !aligned16(k) || !aligned16(qo) || !aligned16(ko) ||
         (wq && !aligned16(wq)) || (wk && !aligned16(wk)) ||
         (rotary_dim > 0 && (!aligned16(rope_cos) || !aligned16(rope_sin))))
         return FA_ERR_ALIGN;
-    p.q = static_cast<const __nv_bfloat16*>(q);
-    p.k = static_cast<const __nv_bfloat16*>(k);
-    p.qo = static_cast<__nv_bfloat16*>(qo);
-    p.ko = static_cast<__nv_bfloat16*>(ko);
-    p.wq = NormWeight{wq, weight_type == FA_WEIGHT_FP32};
-    p.wk = NormWeight{wk, weight_type == FA_WEIGHT_FP32};
+    p.q.x = static_cast<const __nv_bfloat16*>(q);
+    p.k.x = static_cast<const __nv_bfloat16*>(k);
+    p.q.y = static_cast<__nv_bfloat16*>(qo);
+    p.k.y = static_cast<__nv_bfloat16*>(ko);
+    p.q.w = NormWeight{wq, weight_type == FA_WEIGHT_FP32};
+    p.k.w = NormWeight{wk, weight_type == FA_WEIGHT_FP32};
+    p.q.heads = H;
+    p.k.heads = H_kv;
     p.t = RopeTable{rope_cos, rope_sin, max_pos, rotary_dim / 2};
     p.positions = positions;
     p.N = N;
-    p.H = H;
-    p.Hk = H_kv;
+    p.heads_first = layout == FA_LAYOUT_HEADS;
     p.eps = eps;
     return FA_OK;
 }
 
-void set_groups(NormRope& p, int64_t tokens, int heads_per_slot) {
-    p.gq_groups = (p.H + heads_per_slot - 1) / heads_per_slot;
-    p.groups = p.gq_groups + (p.Hk + heads_per_slot - 1) / heads_per_slot;
-    p.slots = tokens * p.groups;
-}
-
-// Workspace of the backward pass: [CTAs, 2, d] partial weight gradients.
-int bwd_ctas(int64_t slots, int d, int num_sms) {
+// Slots of U heads, and CTAs for them: as many as there is work for, up to
+// `per_sm` for each SM, shared between the sides as their slots are.
+int set_grid(NormRope& p, int64_t tokens, int d, int heads_per_slot, int per_sm, int num_sms) {
     const int64_t per = kThreads / (d / 8);
-    const int64_t want = (slots + per - 1) / per, most = static_cast<int64_t>(num_sms) * kBwdCtas;
-    return static_cast<int>(want < most ? want : most);
+    Side* sides[] = {&p.q, &p.k};
+    int64_t want[2];
+    for (int i = 0; i < 2; ++i) {
+        sides[i]->groups = (sides[i]->heads + heads_per_slot - 1) / heads_per_slot;
+        const int64_t slots = tokens * sides[i]->groups;
+        sides[i]->slots = static_cast<uint32_t>(slots);
+        want[i] = (slots + per - 1) / per;
+    }
+    const int64_t most = static_cast<int64_t>(num_sms) * per_sm, all = want[0] + want[1];
+    if (all > most) {
+        int64_t k = (want[1] * most + all / 2) / all;
+        k = k < 1 ? 1 : k > most - 1 ? most - 1 : k;
+        want[1] = k;
+        want[0] = most - k;
+    }
+    p.q.ctas = static_cast<int>(want[0]);
+    p.k.ctas = static_cast<int>(want[1]);
+    return p.q.ctas + p.k.ctas;
 }
 
 template <int D, bool INTER>
-int launch_norm(NormRope& p, int64_t tokens, cudaStream_t st) {
-    constexpr int per = kThreads / (D / 8);
-    set_groups(p, tokens, kFwdHeads);
-    const int64_t ctas = (p.slots + per - 1) / per;
-    fa_norm_rope_kernel<D, INTER, kFwdHeads>
-        <<<static_cast<unsigned>(ctas), kThreads, 0, st>>>(p);
+int launch_norm(const NormRope& p, int ctas, cudaStream_t st) {
+    fa_norm_rope_kernel<D, INTER, kFwdHeads><<<ctas, kThreads, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, bool INTER>
-int launch_norm_bwd(NormRope& p, int ctas, float* dwq, float* dwk, cudaStream_t st) {
+int launch_norm_bwd(const NormRope& p, int ctas, float* dwq, float* dwk, cudaStream_t st) {
     fa_norm_rope_bwd_kernel<D, INTER, kBwdHeads><<<ctas, kThreads, 0, st>>>(p);
     if (p.part)
-        fa_norm_rope_dw_kernel<D><<<2, D * kSumRows, 0, st>>>(p.part, ctas, dwq, dwk);
+        fa_norm_rope_dw_kernel<D><<<2, D * kSumRows, 0, st>>>(p.part, p.q.ctas, ctas, dwq, dwk);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -436,13 +455,14 @@ int fa_qk_norm_rope(const void* q, const void* k, void* q_out, void* k_out, cons
     if (rc != FA_OK) return rc;
     int num_sms = 0;
     if ((rc = fa::device_error_word(&p.err, &num_sms)) != FA_OK) return rc;
-    const int64_t tokens = static_cast<int64_t>(B) * N;
+    const int ctas = fa::set_grid(p, static_cast<int64_t>(B) * N, d, fa::kFwdHeads, fa::kFwdCtas,
+                                  num_sms);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (d == 64)
-        return interleaved ? fa::launch_norm<64, true>(p, tokens, st)
-                           : fa::launch_norm<64, false>(p, tokens, st);
-    return interleaved ? fa::launch_norm<128, true>(p, tokens, st)
-                       : fa::launch_norm<128, false>(p, tokens, st);
+        return interleaved ? fa::launch_norm<64, true>(p, ctas, st)
+                           : fa::launch_norm<64, false>(p, ctas, st);
+    return interleaved ? fa::launch_norm<128, true>(p, ctas, st)
+                       : fa::launch_norm<128, false>(p, ctas, st);
 }
 
 int fa_qk_norm_rope_bwd_workspace(int B, int N, int H, int H_kv, int d, int* bytes) {
@@ -453,10 +473,10 @@ int fa_qk_norm_rope_bwd_workspace(int B, int N, int H, int H_kv, int d, int* byt
     int num_sms = 0, rc;
     if ((rc = fa::device_error_word(&err, &num_sms)) != FA_OK) return rc;
     fa::NormRope p{};
-    p.H = H;
-    p.Hk = H_kv;
-    fa::set_groups(p, static_cast<int64_t>(B) * N, fa::kBwdHeads);
-    *bytes = fa::bwd_ctas(p.slots, d, num_sms) * 2 * d * static_cast<int>(sizeof(float));
+    p.q.heads = H;
+    p.k.heads = H_kv;
+    *bytes = fa::set_grid(p, static_cast<int64_t>(B) * N, d, fa::kBwdHeads, fa::kBwdCtas,
+                          num_sms) * d * static_cast<int>(sizeof(float));
     return FA_OK;
 }
 
@@ -478,21 +498,21 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const 
                       max_pos, rotary_dim, positions, layout, B, N, H, H_kv, d, q_stride,
                       k_stride, dq_stride, dk_stride, eps);
     if (rc != FA_OK) return rc;
-    if ((rc = fa::rows_of(layout, H, N, d, dq_out_stride, &p.rgq)) != FA_OK) return rc;
-    if ((rc = fa::rows_of(layout, H_kv, N, d, dk_out_stride, &p.rgk)) != FA_OK) return rc;
+    if ((rc = fa::rows_of(layout, H, N, d, dq_out_stride, &p.q.rg)) != FA_OK) return rc;
+    if ((rc = fa::rows_of(layout, H_kv, N, d, dk_out_stride, &p.k.rg)) != FA_OK) return rc;
     if (workspace_bytes < 0) return FA_ERR_SHAPE;
     if (!fa::aligned16(dq_out) || !fa::aligned16(dk_out) || !fa::aligned16(workspace))
         return FA_ERR_ALIGN;
-    p.gq = static_cast<const __nv_bfloat16*>(dq_out);
-    p.gk = static_cast<const __nv_bfloat16*>(dk_out);
+    p.q.g = static_cast<const __nv_bfloat16*>(dq_out);
+    p.k.g = static_cast<const __nv_bfloat16*>(dk_out);
     int num_sms = 0;
     if ((rc = fa::device_error_word(&p.err, &num_sms)) != FA_OK) return rc;
-    fa::set_groups(p, static_cast<int64_t>(B) * N, fa::kBwdHeads);
-    const int ctas = fa::bwd_ctas(p.slots, d, num_sms);
+    const int ctas = fa::set_grid(p, static_cast<int64_t>(B) * N, d, fa::kBwdHeads, fa::kBwdCtas,
+                                  num_sms);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (q_weight || k_weight) {
         void* ws = nullptr;
-        const size_t need = sizeof(float) * 2 * static_cast<size_t>(ctas) * d;
+        const size_t need = sizeof(float) * static_cast<size_t>(ctas) * d;
         if ((rc = fa::call_workspace(workspace, workspace_bytes, need, st, &ws)) != FA_OK)
             return rc;
         p.part = static_cast<float*>(ws);
