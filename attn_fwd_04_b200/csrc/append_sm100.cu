@@ -162,26 +162,20 @@ __global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const Append p
         const __nv_bfloat16* x = is_q ? p.q + r * p.sq : is_k ? p.k + r * p.sk : p.v + r * p.sv;
         uint4 raw = make_uint4(0, 0, 0, 0);
         if (live) raw = lane.load(x + static_cast<int64_t>(h) * D);
-        float y[8];
-        unpack8(raw, y);
+        Vec8 y = lane.unpack(raw);
         if (p.wq.w || p.wk.w) {
             const float rs = row_rstd<D>(y, p.eps);
             const NormWeight nw = is_q ? p.wq : p.wk;
-            if (nw.w && (is_q || is_k)) {
-                float w[8];
-                lane.weights(nw, w);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] *= rs * w[j];
-            }
+            if (nw.w && (is_q || is_k)) y = mul8(y, scale8(lane.weights(nw), rs));
         }
         rot.apply(y);
         if (!live) continue;
         if (is_q) {
             lane.store(p.qo + (static_cast<int64_t>(r) * p.H + h) * D,
-                       s.bad ? make_uint4(0, 0, 0, 0) : pack8(y));
+                       s.bad ? make_uint4(0, 0, 0, 0) : lane.pack(y));
         } else if (page >= 0) {
             const int64_t at = ((static_cast<int64_t>(page) * p.Hk + h) * kPage + pos % kPage) * D;
-            if (is_k) lane.store(kp + at, pack8(y));
+            if (is_k) lane.store(kp + at, lane.pack(y));
             else lane.store(vp + at, raw);  // values as they are
         }
     }
@@ -331,19 +325,18 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append p)
         const int pos = s.bad ? 0 : s.len - s.n + (r - s.row0);
         Rotation<D, INTER> rot;
         rot.load(p.t, pos, lane);
-        float w[8];
-        if (p.wq.w) lane.weights(p.wq, w);
+        Vec8 w = {};
+        if (p.wq.w) w = lane.weights(p.wq);
         for (int h = my; h - my < p.H; h += SL) {
             const bool live = h < p.H;
             uint4 raw = make_uint4(0, 0, 0, 0);
             if (live) raw = lane.load(p.q + r * p.sq + static_cast<int64_t>(h) * D);
-            float y[8];
-            unpack8(raw, y);
-            if (p.wq.w) norm_row<D>(y, w, p.eps);
+            Vec8 y = lane.unpack(raw);
+            if (p.wq.w) y = norm_row<D>(y, w, p.eps);
             rot.apply(y);
             if (live)
                 lane.store(p.qo + (static_cast<int64_t>(r) * p.H + h) * D,
-                           s.bad ? make_uint4(0, 0, 0, 0) : pack8(y));
+                           s.bad ? make_uint4(0, 0, 0, 0) : lane.pack(y));
         }
         return;
     }
@@ -361,17 +354,18 @@ __global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append p)
     const __nv_bfloat16* x = (is_k ? p.k : p.v) + static_cast<int64_t>(h) * D;
     const int64_t sx = is_k ? p.sk : p.sv;
     const bool norms = is_k && p.wk.w;
-    float w[8];
-    if (norms) lane.weights(p.wk, w);
+    Vec8 w = {};
+    if (norms) w = lane.weights(p.wk);
     // row `pos` of the new tokens, normed and rotated
     auto row = [&](int pos, float (&y)[8]) {
-        unpack8(lane.load(x + (s.row0 + (pos - start)) * sx), y);
-        if (norms) norm_row<D>(y, w, p.eps);
+        Vec8 v = lane.unpack(lane.load(x + (s.row0 + (pos - start)) * sx));
+        if (norms) v = norm_row<D>(v, w, p.eps);
         if (is_k) {
             Rotation<D, INTER> rot;
             rot.load(p.t, pos, lane);
-            rot.apply(y);
+            rot.apply(v);
         }
+        lane.in_order(v, y);
     };
     float amax = 0.f;
     for (int i = first + my; i - my < last; i += SL) {

@@ -52,13 +52,15 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
     x[7] = bf16_hi(v.w);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
-}
+// A lane's 8 values of a row as 4 pairs of fp32, for the instructions that take
+// two at a time: where the lane is rotated, a[0], a[1] are the first values of
+// its 4 rotation pairs and b[0], b[1] the second.
+struct Vec8 {
+    uint64_t a[2], b[2];
+};
 
-// Which 8 values of a row a lane holds: 4 from `lo` on and 4 from `hi` on; and
-// whether they are 4 pairs of the rotated part.
+// Which 8 values of a row a lane holds: 4 from `lo` on and 4 from `hi` on
+// (interleaved: 8 from `lo` on); and whether they are 4 pairs of the rotated part.
 template <int D, bool INTER>
 struct Lane {
     int chunk, lo, hi;
@@ -100,33 +102,79 @@ struct Lane {
             *reinterpret_cast<uint32_t*>(row + hi) = v.y;
         }
     }
-    // the lane's weights
-    __device__ __forceinline__ void weights(const NormWeight& nw, float (&w)[8]) const {
-        if (nw.fp32) {
-            const float* p = static_cast<const float*>(nw.w);
-            const float4 a = __ldg(reinterpret_cast<const float4*>(p + lo));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(p + hi));
-            w[0] = a.x;
-            w[1] = a.y;
-            w[2] = a.z;
-            w[3] = a.w;
-            w[4] = b.x;
-            w[5] = b.y;
-            w[6] = b.z;
-            w[7] = b.w;
+
+    static __device__ __forceinline__ Vec8 unpack(const uint4& v) {
+        Vec8 x;
+        if (INTER) {
+            x.a[0] = f2_pack(bf16_lo(v.x), bf16_lo(v.y));
+            x.a[1] = f2_pack(bf16_lo(v.z), bf16_lo(v.w));
+            x.b[0] = f2_pack(bf16_hi(v.x), bf16_hi(v.y));
+            x.b[1] = f2_pack(bf16_hi(v.z), bf16_hi(v.w));
         } else {
+            x.a[0] = f2_pack(bf16_lo(v.x), bf16_hi(v.x));
+            x.a[1] = f2_pack(bf16_lo(v.y), bf16_hi(v.y));
+            x.b[0] = f2_pack(bf16_lo(v.z), bf16_hi(v.z));
+            x.b[1] = f2_pack(bf16_lo(v.w), bf16_hi(v.w));
+        }
+        return x;
+    }
+    // The values in the order of the row: `lo` .. lo + 3, then `hi` .. hi + 3.
+    static __device__ __forceinline__ void in_order(const Vec8& x, float (&y)[8]) {
+        if (INTER) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                y[4 * j] = f2_lo(x.a[j]);
+                y[4 * j + 1] = f2_lo(x.b[j]);
+                y[4 * j + 2] = f2_hi(x.a[j]);
+                y[4 * j + 3] = f2_hi(x.b[j]);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                y[2 * j] = f2_lo(x.a[j]);
+                y[2 * j + 1] = f2_hi(x.a[j]);
+                y[4 + 2 * j] = f2_lo(x.b[j]);
+                y[5 + 2 * j] = f2_hi(x.b[j]);
+            }
+        }
+    }
+    static __device__ __forceinline__ Vec8 of(const float (&y)[8]) {
+        Vec8 x;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            x.a[j] = INTER ? f2_pack(y[4 * j], y[4 * j + 2]) : f2_pack(y[2 * j], y[2 * j + 1]);
+            x.b[j] =
+                INTER ? f2_pack(y[4 * j + 1], y[4 * j + 3]) : f2_pack(y[4 + 2 * j], y[5 + 2 * j]);
+        }
+        return x;
+    }
+    static __device__ __forceinline__ uint4 pack(const Vec8& x) {
+        float y[8];
+        in_order(x, y);
+        return make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                          pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+
+    // the lane's weights
+    __device__ __forceinline__ Vec8 weights(const NormWeight& nw) const {
+        if (!nw.fp32) {
             const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(nw.w);
             const uint2 a = __ldg(reinterpret_cast<const uint2*>(p + lo));
             const uint2 b = __ldg(reinterpret_cast<const uint2*>(p + hi));
-            unpack8(make_uint4(a.x, a.y, b.x, b.y), w);
+            return unpack(make_uint4(a.x, a.y, b.x, b.y));
         }
+        const float* p = static_cast<const float*>(nw.w);
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p + lo));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(p + hi));
+        const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        return of(y);
     }
 };
 
 // A position's rotation of a lane's 4 pairs.
 template <int D, bool INTER>
 struct Rotation {
-    float c[4], s[4];
+    uint64_t c[2], s[2];
     bool on;
 
     // pos in [0, max_pos); BACK turns back (the transpose, for gradients)
@@ -140,24 +188,23 @@ struct Rotation {
             cv = __ldg(reinterpret_cast<const float4*>(t.cos_t + at));
             sv = __ldg(reinterpret_cast<const float4*>(t.sin_t + at));
         }
-        c[0] = cv.x;
-        c[1] = cv.y;
-        c[2] = cv.z;
-        c[3] = cv.w;
-        s[0] = BACK ? -sv.x : sv.x;
-        s[1] = BACK ? -sv.y : sv.y;
-        s[2] = BACK ? -sv.z : sv.z;
-        s[3] = BACK ? -sv.w : sv.w;
+        c[0] = f2_pack(cv.x, cv.y);
+        c[1] = f2_pack(cv.z, cv.w);
+        s[0] = BACK ? f2_pack(-sv.x, -sv.y) : f2_pack(sv.x, sv.y);
+        s[1] = BACK ? f2_pack(-sv.z, -sv.w) : f2_pack(sv.z, sv.w);
     }
 
-    __device__ __forceinline__ void apply(float (&y)[8]) const {
+    __device__ __forceinline__ void apply(Vec8& y) const {
         if (!on) return;
+        const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float &a = y[INTER ? 2 * j : j], &b = y[INTER ? 2 * j + 1 : j + 4];
-            const float ra = __fsub_rn(__fmul_rn(a, c[j]), __fmul_rn(b, s[j]));
-            b = __fadd_rn(__fmul_rn(b, c[j]), __fmul_rn(a, s[j]));
-            a = ra;
+        for (int j = 0; j < 2; ++j) {
+            const uint64_t a = y.a[j], b = y.b[j];
+            // products rounded, then their difference (exact times -1) and sum
+            // (one by one: ptxas contracts a packed sum of packed products)
+            y.a[j] = f2_fma(f2_mul(b, s[j]), minus, f2_mul(a, c[j]));
+            const uint64_t bc = f2_mul(b, c[j]), as = f2_mul(a, s[j]);
+            y.b[j] = f2_pack(__fadd_rn(f2_lo(bc), f2_lo(as)), __fadd_rn(f2_hi(bc), f2_hi(as)));
         }
     }
 };
@@ -170,21 +217,45 @@ __device__ __forceinline__ float row_sum(float v) {
     return v;
 }
 
-// 1 / sqrt(mean(x^2) + eps) of a row.
-template <int D>
-__device__ __forceinline__ float row_rstd(const float (&x)[8], float eps) {
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-    return rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
+__device__ __forceinline__ float dot8(const Vec8& x, const Vec8& y) {
+    uint64_t d = f2_mul(x.a[0], y.a[0]);
+    d = f2_fma(x.a[1], y.a[1], d);
+    d = f2_fma(x.b[0], y.b[0], d);
+    d = f2_fma(x.b[1], y.b[1], d);
+    return f2_lo(d) + f2_hi(d);
 }
 
-// x normed by the lane's weights, in place (every lane of the row together).
-template <int D>
-__device__ __forceinline__ void norm_row(float (&x)[8], const float (&w)[8], float eps) {
-    const float r = row_rstd<D>(x, eps);
+__device__ __forceinline__ Vec8 mul8(const Vec8& x, const Vec8& y) {
+    Vec8 z;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] *= r * w[j];
+    for (int j = 0; j < 2; ++j) {
+        z.a[j] = f2_mul(x.a[j], y.a[j]);
+        z.b[j] = f2_mul(x.b[j], y.b[j]);
+    }
+    return z;
+}
+
+__device__ __forceinline__ Vec8 scale8(const Vec8& x, float r) {
+    const uint64_t rr = f2_pack(r, r);
+    Vec8 z;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        z.a[j] = f2_mul(x.a[j], rr);
+        z.b[j] = f2_mul(x.b[j], rr);
+    }
+    return z;
+}
+
+// 1 / sqrt(mean(x^2) + eps) of a row.
+template <int D>
+__device__ __forceinline__ float row_rstd(const Vec8& x, float eps) {
+    return rsqrtf(fmaf(row_sum<D>(dot8(x, x)), 1.f / D, eps));
+}
+
+// x normed by the lane's weights (every lane of the row together).
+template <int D>
+__device__ __forceinline__ Vec8 norm_row(const Vec8& x, const Vec8& w, float eps) {
+    return mul8(x, scale8(w, row_rstd<D>(x, eps)));
 }
 
 }  // namespace fa

@@ -83,6 +83,22 @@ struct Rows {
     }
 };
 
+// i / d for i < 2^31 by a multiplication (Granlund and Montgomery, "Division by
+// Invariant Integers using Multiplication", 1994): with l = ceil(log2 d) and
+// m = floor(2^32 (2^l - d) / d) + 1, it is (floor(m i / 2^32) + i) >> l.
+struct Divisor {
+    uint32_t d, m, l;
+    static Divisor of(uint32_t d) {
+        uint32_t l = 0;
+        while ((uint64_t{1} << l) < d) ++l;
+        const uint64_t m = ((uint64_t{1} << 32) * ((uint64_t{1} << l) - d)) / d + 1;
+        return Divisor{d, static_cast<uint32_t>(m), l};
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t i) const {
+        return (__umulhi(m, i) + i) >> l;
+    }
+};
+
 // One of the two tensors of a call: queries or keys.
 struct Side {
     const __nv_bfloat16* x;  // the rows to norm
@@ -90,16 +106,17 @@ struct Side {
     __nv_bfloat16* y;        // outputs, or gradients of the rows
     Rows rx, rg, ry;
     NormWeight w;
-    int heads, groups;  // groups of U heads
-    uint32_t slots;     // tokens * groups
-    int ctas;           // CTAs of the grid that take this side
+    int heads;
+    Divisor groups;  // groups of U heads
+    uint32_t slots;  // tokens * groups
+    int ctas;        // CTAs of the grid that take this side
 };
 
 struct NormRope {
     Side q, k;
     RopeTable t;
     const int32_t* positions;
-    int N;
+    Divisor N;
     bool heads_first;
     float eps;
     float* part;  // backward: [CTAs, D] partial weight gradients
@@ -114,19 +131,20 @@ struct Slot {
     int b, n, h0;
     __device__ __forceinline__ Slot(const NormRope& p, const Side& s, uint32_t i, int U) {
         if (p.heads_first) {
-            const uint32_t outer = i / static_cast<uint32_t>(p.N);
-            n = static_cast<int>(i - outer * p.N);
-            b = static_cast<int>(outer / static_cast<uint32_t>(s.groups));
-            h0 = static_cast<int>(outer - static_cast<uint32_t>(b) * s.groups) * U;
+            const uint32_t outer = p.N.quotient(i);
+            n = static_cast<int>(i - outer * p.N.d);
+            b = static_cast<int>(s.groups.quotient(outer));
+            h0 = static_cast<int>(outer - static_cast<uint32_t>(b) * s.groups.d) * U;
         } else {
             b = 0;
-            n = static_cast<int>(i / static_cast<uint32_t>(s.groups));
-            h0 = static_cast<int>(i - static_cast<uint32_t>(n) * s.groups) * U;
+            n = static_cast<int>(s.groups.quotient(i));
+            h0 = static_cast<int>(i - static_cast<uint32_t>(n) * s.groups.d) * U;
         }
     }
     // The token's position in the tables; out of them: 0, and bad.
     __device__ __forceinline__ int position(const NormRope& p, bool& bad) const {
-        const int pos = p.positions ? __ldg(p.positions + static_cast<int64_t>(b) * p.N + n) : n;
+        const int pos =
+            p.positions ? __ldg(p.positions + static_cast<int64_t>(b) * p.N.d + n) : n;
         bad = p.t.half > 0 && (pos < 0 || pos >= p.t.max_pos);
         return bad ? 0 : pos;
     }
@@ -142,34 +160,36 @@ __global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const __grid_con
     const Side& s = is_q ? p.q : p.k;
     const uint32_t stride = static_cast<uint32_t>(s.ctas) * SL;
     const bool norms = s.w.w != nullptr;
-    float w[8];
-    if (norms) lane.weights(s.w, w);
+    Vec8 w = {};
+    if (norms) w = lane.weights(s.w);
     // all lanes of a warp stay together: the last slot stands in for those behind it
     for (uint32_t base = (blockIdx.x - (is_q ? 0 : p.q.ctas)) * SL; base < s.slots;
          base += stride) {
         const uint32_t i = base + threadIdx.x / LPR;
         const bool live = i < s.slots;
         const Slot at(p, s, live ? i : s.slots - 1, U);
+        const int count = s.heads - at.h0;  // of rows, U at most
         uint4 raw[U];
+        const __nv_bfloat16* x = s.x + s.rx.at(at.b, at.n, at.h0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             raw[u] = make_uint4(0, 0, 0, 0);
-            if (at.h0 + u < s.heads) raw[u] = lane.load(s.x + s.rx.at(at.b, at.n, at.h0 + u));
+            if (u < count) raw[u] = lane.load(x);
+            x += s.rx.head;
         }
         bool bad;
         const int pos = at.position(p, bad);
         if (bad && live && lane.chunk == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
         Rotation<D, INTER> rot;
         rot.load(p.t, pos, lane);
+        __nv_bfloat16* y = s.y + s.ry.at(at.b, at.n, at.h0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float v[8];
-            unpack8(raw[u], v);
-            if (norms) norm_row<D>(v, w, p.eps);
+            Vec8 v = lane.unpack(raw[u]);
+            if (norms) v = norm_row<D>(v, w, p.eps);
             rot.apply(v);
-            if (live && at.h0 + u < s.heads)
-                lane.store(s.y + s.ry.at(at.b, at.n, at.h0 + u),
-                           bad ? make_uint4(0, 0, 0, 0) : pack8(v));
+            if (live && u < count) lane.store(y, bad ? make_uint4(0, 0, 0, 0) : lane.pack(v));
+            y += s.ry.head;
         }
     }
 }
@@ -189,62 +209,71 @@ __global__ void __launch_bounds__(kThreads)
     const Side& s = is_q ? p.q : p.k;
     const uint32_t stride = static_cast<uint32_t>(s.ctas) * SL;
     const bool norms = s.w.w != nullptr;
-    float w[8], acc[8];
-    if (norms) lane.weights(s.w, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+    Vec8 w = {}, acc = {};
+    if (norms) w = lane.weights(s.w);
     for (uint32_t base = (blockIdx.x - (is_q ? 0 : p.q.ctas)) * SL; base < s.slots;
          base += stride) {
         const uint32_t i = base + threadIdx.x / LPR;
         const bool live = i < s.slots;
         const Slot at(p, s, live ? i : s.slots - 1, U);
+        const int count = s.heads - at.h0;
         uint4 gr[U], xr[U];
+        const __nv_bfloat16* g = s.g + s.rg.at(at.b, at.n, at.h0);
+        const __nv_bfloat16* x = s.x + s.rx.at(at.b, at.n, at.h0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             gr[u] = xr[u] = make_uint4(0, 0, 0, 0);
-            if (at.h0 + u < s.heads) {
-                gr[u] = lane.load(s.g + s.rg.at(at.b, at.n, at.h0 + u));
-                if (norms) xr[u] = lane.load(s.x + s.rx.at(at.b, at.n, at.h0 + u));
+            if (u < count) {
+                gr[u] = lane.load(g);
+                if (norms) xr[u] = lane.load(x);
             }
+            g += s.rg.head;
+            x += s.rx.head;
         }
         bool bad;
         const int pos = at.position(p, bad);
         if (bad && live && lane.chunk == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
         Rotation<D, INTER> rot;
         rot.template load<true>(p.t, pos, lane);
+        __nv_bfloat16* y = s.y + s.ry.at(at.b, at.n, at.h0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            float gv[8];
-            unpack8(gr[u], gv);
+            Vec8 gv = lane.unpack(gr[u]);
             rot.apply(gv);
-            const bool mine = live && at.h0 + u < s.heads;
+            const bool mine = live && u < count;
             if (norms) {
-                float xv[8];
-                unpack8(xr[u], xv);
-                const float r = row_rstd<D>(xv, p.eps);
-                float dot = 0.f;
+                Vec8 hat = lane.unpack(xr[u]);
+                const float r = row_rstd<D>(hat, p.eps);
+                hat = scale8(hat, r);
+                if (mine && !bad) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    xv[j] *= r;
-                    if (mine && !bad) acc[j] = fmaf(gv[j], xv[j], acc[j]);
-                    gv[j] *= w[j];
-                    dot = fmaf(gv[j], xv[j], dot);
+                    for (int j = 0; j < 2; ++j) {
+                        acc.a[j] = f2_fma(gv.a[j], hat.a[j], acc.a[j]);
+                        acc.b[j] = f2_fma(gv.b[j], hat.b[j], acc.b[j]);
+                    }
                 }
-                dot = row_sum<D>(dot) * (1.f / D);
+                gv = mul8(gv, w);
+                const float m = -row_sum<D>(dot8(gv, hat)) * (1.f / D);
+                const uint64_t mm = f2_pack(m, m);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) gv[j] = r * (gv[j] - xv[j] * dot);
+                for (int j = 0; j < 2; ++j) {
+                    gv.a[j] = f2_fma(hat.a[j], mm, gv.a[j]);
+                    gv.b[j] = f2_fma(hat.b[j], mm, gv.b[j]);
+                }
+                gv = scale8(gv, r);
             }
-            if (mine)
-                lane.store(s.y + s.ry.at(at.b, at.n, at.h0 + u),
-                           bad ? make_uint4(0, 0, 0, 0) : pack8(gv));
+            if (mine) lane.store(y, bad ? make_uint4(0, 0, 0, 0) : lane.pack(gv));
+            y += s.ry.head;
         }
     }
     if (!norms) return;  // the whole CTA
+    float sums[8];
+    lane.in_order(acc, sums);
     const int my = threadIdx.x / LPR;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        red[my][lane.lo + j] = acc[j];
-        red[my][lane.hi + j] = acc[4 + j];
+        red[my][lane.lo + j] = sums[j];
+        red[my][lane.hi + j] = sums[4 + j];
     }
     __syncthreads();
     if (threadIdx.x < D) {
@@ -284,7 +313,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 constexpr int kFwdHeads = 4;  // heads a slot takes
 constexpr int kBwdHeads = 2;
 constexpr int kFwdCtas = 32;  // CTAs per SM of the grids, at most
-constexpr int kBwdCtas = 4;
+constexpr int kBwdCtas = 3;
 
 // The rows of a tensor with `heads` heads: packed tokens `stride` apart (0:
 // back to back), or [B, heads, N, d].
@@ -340,7 +369,7 @@ int fill(NormRope& p, const void* q, const void* k, void* qo, void* ko, const vo
     p.k.heads = H_kv;
     p.t = RopeTable{rope_cos, rope_sin, max_pos, rotary_dim / 2};
     p.positions = positions;
-    p.N = N;
+    p.N = Divisor::of(static_cast<uint32_t>(N));
     p.heads_first = layout == FA_LAYOUT_HEADS;
     p.eps = eps;
     return FA_OK;
@@ -353,8 +382,9 @@ int set_grid(NormRope& p, int64_t tokens, int d, int heads_per_slot, int per_sm,
     Side* sides[] = {&p.q, &p.k};
     int64_t want[2];
     for (int i = 0; i < 2; ++i) {
-        sides[i]->groups = (sides[i]->heads + heads_per_slot - 1) / heads_per_slot;
-        const int64_t slots = tokens * sides[i]->groups;
+        const int groups = (sides[i]->heads + heads_per_slot - 1) / heads_per_slot;
+        sides[i]->groups = Divisor::of(static_cast<uint32_t>(groups));
+        const int64_t slots = tokens * groups;
         sides[i]->slots = static_cast<uint32_t>(slots);
         want[i] = (slots + per - 1) / per;
     }
