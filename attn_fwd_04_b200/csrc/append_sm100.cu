@@ -9,10 +9,10 @@
 // output to what attention reads: queries rotated, keys rotated and stored,
 // values stored.  Each row is read and written once.
 //
-// Each CTA finds its own sequence: its threads look at the sequences' offsets
-// and lengths together, one sequence a thread, and the block sums the pages
-// before it.  That is one round trip to L2, overlapped with the loads of the
-// rows, where a plan kernel before it would be a launch of its own.
+// Each CTA finds its own sequences: its threads look at all offsets and
+// lengths together, one sequence a thread, and scan the pages before them.
+// That is one round trip to L2, overlapped with the loads of the rows and
+// shared by the CTA's tokens, where a plan kernel would be a launch of its own.
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -24,8 +24,10 @@ namespace fa {
 namespace {
 
 constexpr int kPage = 256;
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kTokens = 16;  // of a CTA, at most, where rows are taken one by one
+constexpr int kRows = 4;     // a thread has in flight
 
 struct Append {
     const __nv_bfloat16 *q, *k, *v;  // new rows, `stride` elements a token apart
@@ -39,7 +41,9 @@ struct Append {
     NormWeight wq, wk;
     RopeTable t;
     int B, H, Hk, total, num_pages;
-    int units;  // 8-bit: (sequence, block) pairs with new rows, at most
+    int tokens;  // of a CTA that takes rows
+    int units;   // 8-bit: (sequence, block) pairs with new rows, at most
+    int unit_heads, unit_ctas;  // heads of a CTA that takes a unit; such CTAs
     float eps;
     unsigned int* err;
 };
@@ -64,19 +68,6 @@ __device__ __forceinline__ void rows_of(const Append& p, int b, int& r0, int& n,
     bad = lo < 0 || hi > p.total || hi < lo;
     r0 = min(max(lo, 0), p.total);
     n = bad ? 0 : hi - lo;
-}
-
-// Sum over the block (every thread gets it).
-__device__ __forceinline__ int64_t block_sum(int64_t a, int64_t* sh /*[kWarps]*/) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = a;
-    __syncthreads();
-    int64_t s = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) s += sh[i];
-    __syncthreads();
-    return s;
 }
 
 // Whether the sequence's new rows fit it, its table row and the rotation's
@@ -104,81 +95,171 @@ struct Shared {
     int64_t units[kWarps], pages[kWarps];
     int64_t page_base;
     int b, blk;
+    // rows: of each token, its sequence, that one's page base; position and page
+    int seq[kTokens];
+    int64_t base[kTokens];
+    int pos[kTokens], page[kTokens];
 };
 
-// The sequence that holds row r, found by the whole CTA.
-__device__ __forceinline__ Seq find_row(const Append& p, int r, Shared& sh) {
-    if (threadIdx.x == 0) sh.b = -1;
-    __syncthreads();
-    int mine = -1;
-    for (int i = threadIdx.x; i < p.B; i += kThreads) {
-        int r0, n;
-        bool bad;
-        rows_of(p, i, r0, n, bad);
-        if (r >= r0 && r < r0 + n) mine = i;
-        if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
+// Exclusive prefix over the block; `total` of it.
+__device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t* sh /*[kWarps]*/,
+                                                int64_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t n = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += n;
     }
-    if (mine >= 0) atomicMax(&sh.b, mine);  // offsets that overlap: the last one
+    if (lane == 31) sh[warp] = inc;
     __syncthreads();
-    Seq s{};
-    s.b = sh.b;
-    s.found = s.b >= 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) inc += sh[w];
+        total += sh[w];
+    }
+    __syncthreads();
+    return inc - v;
+}
+
+// Where rows first .. first + count - 1 belong: sh.pos (-1: of a sequence that
+// cannot be taken) and sh.page (-1: nothing is stored); sh.seq -1: a row of no
+// sequence, left alone.
+__device__ __forceinline__ void place_rows(const Append& p, int first, int count, Shared& sh) {
+    if (threadIdx.x < kTokens) sh.seq[threadIdx.x] = -1;
+    __syncthreads();
     int64_t pages = 0;
-    if (!p.max_pages)
-        for (int i = threadIdx.x; i < s.b; i += kThreads) pages += pages_of(__ldg(p.lens + i));
-    s.page_base = block_sum(pages, sh.pages);
-    if (!s.found) return s;
-    rows_of(p, s.b, s.row0, s.n, s.bad);
-    s.len = __ldg(p.lens + s.b);
-    s.bad = s.bad || seq_bad(p, s.n, s.len, s.page_base);
-    if (s.bad && threadIdx.x == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
-    return s;
+    for (int at = 0; at < p.B; at += kThreads) {
+        const int i = at + threadIdx.x;
+        int r0 = 0, n = 0, len = 0;
+        if (i < p.B) {
+            bool bad;
+            rows_of(p, i, r0, n, bad);
+            len = __ldg(p.lens + i);
+            if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
+        }
+        const int lo = max(r0, first), hi = min(r0 + n, first + count);
+        for (int r = lo; r < hi; ++r) atomicMax(&sh.seq[r - first], i);  // overlapping: the last
+        int64_t base = 0, total = 0;
+        if (p.max_pages) {
+            __syncthreads();
+        } else {
+            base = pages + block_prefix(pages_of(len), sh.pages, total);
+            pages += total;
+        }
+        for (int r = lo; r < hi; ++r)
+            if (sh.seq[r - first] == i) sh.base[r - first] = base;
+    }
+    __syncthreads();
+    if (threadIdx.x < count && sh.seq[threadIdx.x] >= 0) {
+        Seq s{};
+        s.b = sh.seq[threadIdx.x];
+        rows_of(p, s.b, s.row0, s.n, s.bad);
+        s.len = __ldg(p.lens + s.b);
+        s.page_base = sh.base[threadIdx.x];
+        int pos = -1, page = -1;
+        if (seq_bad(p, s.n, s.len, s.page_base)) {
+            record_error(p.err, FA_DEVERR_BAD_INPUT);
+        } else {
+            pos = s.len - s.n + (first + static_cast<int>(threadIdx.x) - s.row0);
+            page = page_at(p, s, pos);
+        }
+        sh.pos[threadIdx.x] = pos;
+        sh.page[threadIdx.x] = page;
+    }
+    __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
-// bf16 pages: a CTA takes one token; D / 8 lanes a row of it, the H query
-// rows, H_kv key rows and H_kv value rows in turn.
+// Rows one by one: the queries, and into bf16 pages the keys and values.  A
+// slot is kRows heads of one token and kind, taken by D / 8 lanes; the next
+// slot's rows are on their way while one is worked on, the first ones while
+// the CTA looks for its sequences.
 // ---------------------------------------------------------------------------
-template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const Append p) {
+template <int D, bool INTER, bool KV>
+__device__ __forceinline__ void append_rows(const Append& p, int cta, Shared& sh) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
-    __shared__ Shared sh;
-    const int r = blockIdx.x;
-    const int my = threadIdx.x / LPR;
-    const Seq s = find_row(p, r, sh);
-    if (!s.found) return;
-    const int pos = s.bad ? 0 : s.len - s.n + (r - s.row0);
-    const int page = s.bad ? -1 : page_at(p, s, pos);
     const Lane<D, INTER> lane(p.t.half);
-    Rotation<D, INTER> rot;
-    rot.load(p.t, pos, lane);
-    __nv_bfloat16* kp = static_cast<__nv_bfloat16*>(p.kp);
-    __nv_bfloat16* vp = static_cast<__nv_bfloat16*>(p.vp);
-    const int rows = p.H + 2 * p.Hk;
-    for (int i = my; i - my < rows; i += SL) {
-        const bool live = i < rows;
-        const bool is_q = i < p.H, is_k = !is_q && i < p.H + p.Hk;
-        const int h = is_q ? i : is_k ? i - p.H : min(i - p.H - p.Hk, p.Hk - 1);
-        const __nv_bfloat16* x = is_q ? p.q + r * p.sq : is_k ? p.k + r * p.sk : p.v + r * p.sv;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (live) raw = lane.load(x + static_cast<int64_t>(h) * D);
-        Vec8 y = lane.unpack(raw);
-        if (p.wq.w || p.wk.w) {
-            const float rs = row_rstd<D>(y, p.eps);
-            const NormWeight nw = is_q ? p.wq : p.wk;
-            if (nw.w && (is_q || is_k)) y = mul8(y, scale8(lane.weights(nw), rs));
+    const int my = threadIdx.x / LPR;
+    const int first = cta * p.tokens, count = min(p.tokens, p.total - first);
+    const int gq = (p.H + kRows - 1) / kRows, gk = KV ? (p.Hk + kRows - 1) / kRows : 0;
+    const int groups = gq + 2 * gk, slots = count * groups;
+    struct Where {
+        int tok, kind, h0, rows;  // kind 0: query, 1: key, 2: value
+    };
+    auto where = [&](int i) {
+        Where w;
+        w.tok = i / groups;
+        const int g = i - w.tok * groups;
+        w.kind = g < gq ? 0 : g < gq + gk ? 1 : 2;
+        w.h0 = (w.kind == 0 ? g : w.kind == 1 ? g - gq : g - gq - gk) * kRows;
+        w.rows = i < slots ? min(kRows, (w.kind == 0 ? p.H : p.Hk) - w.h0) : 0;
+        return w;
+    };
+    uint4 next[kRows];
+    auto fetch = [&](const Where& w) {
+        const int64_t r = first + w.tok;
+        const __nv_bfloat16* x = (w.kind == 0   ? p.q + r * p.sq
+                                  : w.kind == 1 ? p.k + r * p.sk
+                                                : p.v + r * p.sv) + static_cast<int64_t>(w.h0) * D;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+            if (u < w.rows) next[u] = lane.load(x + u * D);
+    };
+    Where w = where(my);
+    fetch(w);
+    place_rows(p, first, count, sh);
+    const bool norms = p.wq.w || p.wk.w;
+    for (int i = my; i - my < slots; i += SL) {  // all lanes of a warp together
+        uint4 raw[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) raw[u] = next[u];
+        const Where now = w;
+        w = where(i + SL);
+        fetch(w);
+        if (now.rows == 0 && !norms) continue;
+        const int tok = min(now.tok, count - 1);
+        const bool mine = sh.seq[tok] >= 0;
+        const int pos = mine ? sh.pos[tok] : -1, page = mine ? sh.page[tok] : -1;
+        Rotation<D, INTER> rot;
+        rot.load(p.t, max(pos, 0), lane);
+        const NormWeight nw = now.kind == 0 ? p.wq : now.kind == 1 ? p.wk : NormWeight{nullptr, 0};
+        Vec8 weight = {};
+        if (nw.w) weight = lane.weights(nw);
+        __nv_bfloat16* y;
+        int64_t step;
+        bool store = mine;
+        if (now.kind == 0) {
+            y = p.qo + (static_cast<int64_t>(first + tok) * p.H + now.h0) * D;
+            step = D;
+        } else {
+            y = static_cast<__nv_bfloat16*>(now.kind == 1 ? p.kp : p.vp) +
+                ((static_cast<int64_t>(page) * p.Hk + now.h0) * kPage + pos % kPage) * D;
+            step = kPage * D;
+            store = page >= 0;
         }
-        rot.apply(y);
-        if (!live) continue;
-        if (is_q) {
-            lane.store(p.qo + (static_cast<int64_t>(r) * p.H + h) * D,
-                       s.bad ? make_uint4(0, 0, 0, 0) : lane.pack(y));
-        } else if (page >= 0) {
-            const int64_t at = ((static_cast<int64_t>(page) * p.Hk + h) * kPage + pos % kPage) * D;
-            if (is_k) lane.store(kp + at, lane.pack(y));
-            else lane.store(vp + at, raw);  // values as they are
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            if (u >= now.rows) raw[u] = make_uint4(0, 0, 0, 0);
+            Vec8 v = lane.unpack(raw[u]);
+            if (norms) {  // the same for the launch; a warp's slots may be of two kinds
+                const float r = row_rstd<D>(v, p.eps);
+                if (nw.w) v = mul8(v, scale8(weight, r));
+            }
+            rot.apply(v);
+            const uint4 out = now.kind == 2 ? raw[u]  // values as they are
+                              : pos < 0     ? make_uint4(0, 0, 0, 0)
+                                            : lane.pack(v);
+            if (store && u < now.rows) lane.store(y + u * step, out);
         }
     }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const __grid_constant__ Append p) {
+    __shared__ Shared sh;
+    append_rows<D, INTER, true>(p, blockIdx.x, sh);
 }
 
 // ---------------------------------------------------------------------------
@@ -188,7 +269,13 @@ __global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const Append p
 // format's normal range.  With a the largest finite magnitude of the block's
 // new values, the scale is the least 2^e with a <= 448 * 2^e (e in [-64, 64]),
 // or the block's present scale where it holds earlier tokens and that is
-// larger.  A CTA takes one (sequence, block) and one head of K or of V.
+// larger.
+//
+// A CTA takes one (sequence, block) of K or of V and some of its heads, one
+// after the other.  Each thread keeps its rows' values in registers between
+// the maximum and the rounding (4 rows: 64 tokens of 128 values a CTA; larger
+// blocks are read twice), and its positions' rotations for all heads; the next
+// head's rows are on their way meanwhile.
 // ---------------------------------------------------------------------------
 constexpr float kMaxCode = 448.f;
 
@@ -199,31 +286,13 @@ __device__ __forceinline__ int scale_exponent(float a) {
     return a > 0.f ? min(max(e - 9 + (m > 0.875f), -64), 64) : -64;
 }
 
-// y / scale.  The inverse of a power of two is exact (2^-64 .. 2^64), so the
-// product is the quotient; a caller's other scale divides.
-__device__ __forceinline__ void divide8(float (&y)[8], float scale) {
-    if ((__float_as_uint(scale) & 0x7fffffu) == 0) {  // the same for the CTA
-        const float inv = 1.f / scale;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] *= inv;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(y[j], scale);
-    }
-}
-
-// 8-bit codes of values already divided by the scale: to nearest even; what
-// the format cannot hold is stored as NaN, so that it shows.
-__device__ __forceinline__ float codable(float v) {
-    return fabsf(v) <= kMaxCode ? v : __int_as_float(0x7fffffff);
-}
-
+// 8-bit codes of values already divided by the scale: to nearest even.
 __device__ __forceinline__ uint2 encode8(const float (&y)[8]) {
     uint32_t h[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        h[j] = __nv_cvt_float2_to_fp8x2(make_float2(codable(y[2 * j]), codable(y[2 * j + 1])),
-                                        __NV_SATFINITE, __NV_E4M3);
+        h[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * j], y[2 * j + 1]), __NV_SATFINITE,
+                                        __NV_E4M3);
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
@@ -309,105 +378,156 @@ __device__ __forceinline__ bool find_unit(const Append& p, int unit, Shared& sh,
     return !s.bad;
 }
 
+// Largest magnitude of a lane's values, infinities among them, NaN not.
+__device__ __forceinline__ float largest8(const Vec8& v) {
+    float m = fmaxf(fabsf(f2_lo(v.a[0])), fabsf(f2_hi(v.a[0])));
+    m = max3f(m, fabsf(f2_lo(v.a[1])), fabsf(f2_hi(v.a[1])));
+    m = max3f(m, fabsf(f2_lo(v.b[0])), fabsf(f2_hi(v.b[0])));
+    return max3f(m, fabsf(f2_lo(v.b[1])), fabsf(f2_hi(v.b[1])));
+}
+
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) fa_append_fp8_kernel(const Append p) {
-    constexpr int LPR = D / 8, SL = kThreads / LPR;
-    __shared__ Shared sh;
-    __shared__ float red[kWarps];
-    const int my = threadIdx.x / LPR;
+__device__ __forceinline__ void append_block(const Append& p, int cta, Shared& sh) {
+    constexpr int LPR = D / 8, SL = kThreads / LPR, CH = SL * kRows;  // tokens at a time
+    __shared__ float red[2][kWarps];
     const Lane<D, INTER> lane(p.t.half);
-    const int kv_ctas = p.units * 2 * p.Hk;
-    if (static_cast<int>(blockIdx.x) >= kv_ctas) {
-        // query rows: one token's heads over a CTA's slots
-        const int r = blockIdx.x - kv_ctas;
-        const Seq s = find_row(p, r, sh);
-        if (!s.found) return;
-        const int pos = s.bad ? 0 : s.len - s.n + (r - s.row0);
-        Rotation<D, INTER> rot;
-        rot.load(p.t, pos, lane);
-        Vec8 w = {};
-        if (p.wq.w) w = lane.weights(p.wq);
-        for (int h = my; h - my < p.H; h += SL) {
-            const bool live = h < p.H;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (live) raw = lane.load(p.q + r * p.sq + static_cast<int64_t>(h) * D);
-            Vec8 y = lane.unpack(raw);
-            if (p.wq.w) y = norm_row<D>(y, w, p.eps);
-            rot.apply(y);
-            if (live)
-                lane.store(p.qo + (static_cast<int64_t>(r) * p.H + h) * D,
-                           s.bad ? make_uint4(0, 0, 0, 0) : lane.pack(y));
-        }
-        return;
-    }
-    const int unit = blockIdx.x / (2 * p.Hk), sub = blockIdx.x - unit * 2 * p.Hk;
-    const bool is_k = sub < p.Hk;
-    const int h = is_k ? sub : sub - p.Hk;
+    const int my = threadIdx.x / LPR;
+    const int hgroups = (p.Hk + p.unit_heads - 1) / p.unit_heads;
+    const int unit = cta / (2 * hgroups), sub = cta - unit * 2 * hgroups;
+    const bool is_k = sub < hgroups;
+    const int h_begin = (is_k ? sub : sub - hgroups) * p.unit_heads;
+    const int h_end = min(h_begin + p.unit_heads, p.Hk);
     Seq s;
     int blk = 0;
     if (!find_unit(p, unit, sh, s, blk)) return;
     const int lg = p.block_log2, start = s.len - s.n;
-    const int lo = blk << lg;                              // the block's first position
+    const int lo = blk << lg;  // the block's first position
     const int first = max(lo, start), last = min(lo + (1 << lg), s.len);
     const int page = page_at(p, s, lo);
     if (page < 0) return;
-    const __nv_bfloat16* x = (is_k ? p.k : p.v) + static_cast<int64_t>(h) * D;
-    const int64_t sx = is_k ? p.sk : p.sv;
+    const int chunks = (last - first + CH - 1) / CH;
     const bool norms = is_k && p.wk.w;
     Vec8 w = {};
     if (norms) w = lane.weights(p.wk);
-    // row `pos` of the new tokens, normed and rotated
-    auto row = [&](int pos, float (&y)[8]) {
-        Vec8 v = lane.unpack(lane.load(x + (s.row0 + (pos - start)) * sx));
-        if (norms) v = norm_row<D>(v, w, p.eps);
-        if (is_k) {
-            Rotation<D, INTER> rot;
-            rot.load(p.t, pos, lane);
-            rot.apply(v);
+    Rotation<D, INTER> rot[kRows];
+    int turned = -1;  // the chunk that `rot` is of
+    const int64_t sx = is_k ? p.sk : p.sv;
+    const __nv_bfloat16* x0 = (is_k ? p.k : p.v) + (s.row0 + (first - start)) * sx;
+    uint4 raw[kRows];
+    auto fetch = [&](int h, int c) {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const int r = c * CH + u * SL + my;
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (first + r < last) raw[u] = lane.load(x0 + r * sx + static_cast<int64_t>(h) * D);
         }
-        lane.in_order(v, y);
     };
-    float amax = 0.f;
-    for (int i = first + my; i - my < last; i += SL) {
-        float y[8];
-        row(min(i, last - 1), y);
+    Vec8 v[kRows];
+    auto values = [&](int c) {  // of the rows in `raw`, normed and rotated
+        if (is_k && turned != c) {
+            turned = c;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float a = fabsf(y[j]);
-            if (a < INFINITY) amax = fmaxf(amax, a);
+            for (int u = 0; u < kRows; ++u)
+                rot[u].load(p.t, min(first + c * CH + u * SL + my, last - 1), lane);
         }
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-    const int64_t slice = static_cast<int64_t>(page) * p.Hk + h;
-    float* scale = (is_k ? p.ks : p.vs) + slice * (kPage >> lg) + ((lo % kPage) >> lg);
-    const float was = first > lo ? *scale : 0.f;
-    __syncthreads();  // every thread has read the old scale
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) amax = fmaxf(amax, red[i]);
-    const int e = scale_exponent(amax);
-    const float now = fmaxf(was, ldexpf(1.f, e));
-    uint8_t* dst = static_cast<uint8_t*>(is_k ? p.kp : p.vp) +
-                   (slice * kPage + lo % kPage) * D;
-    if (threadIdx.x == 0) *scale = now;
-    if (first > lo && now != was) {  // earlier tokens under the larger scale
-        const float ratio = was / now;  // now is a power of two
-        for (int i = my; i < first - lo; i += SL) {
-            float y[8];
-            uint8_t* c = dst + static_cast<int64_t>(i) * D;
-            decode8(lane.load(c), y);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= ratio;
-            lane.store(c, encode8(y));
+        for (int u = 0; u < kRows; ++u) {
+            v[u] = lane.unpack(raw[u]);
+            if (norms) v[u] = norm_row<D>(v[u], w, p.eps);
+            if (is_k) rot[u].apply(v[u]);
         }
+    };
+    fetch(h_begin, 0);
+    for (int h = h_begin; h < h_end; ++h) {
+        // ---- the largest finite magnitude; `odd`: infinities too -------------------
+        float amax = 0.f, odd = 0.f;
+        for (int c = 0; c < chunks; ++c) {
+            if (c > 0) fetch(h, c);
+            values(c);
+            float m = 0.f;
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) m = fmaxf(m, largest8(v[u]));
+            odd = fmaxf(odd, m);
+            if (m == INFINITY) {  // rare: once more without them
+                m = 0.f;
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) {
+                    float y[8];
+                    lane.in_order(v[u], y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (fabsf(y[j]) < INFINITY) m = fmaxf(m, fabsf(y[j]));
+                }
+            }
+            amax = fmaxf(amax, m);
+        }
+        if (chunks == 1 && h + 1 < h_end) fetch(h + 1, 0);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        float* mine = red[h & 1];  // two, so that one barrier a head will do
+        if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = amax;
+        const int64_t slice = static_cast<int64_t>(page) * p.Hk + h;
+        float* scale = (is_k ? p.ks : p.vs) + slice * (kPage >> lg) + ((lo % kPage) >> lg);
+        const float was = first > lo ? *scale : 0.f;
+        __syncthreads();  // every thread has read the old scale
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) amax = fmaxf(amax, mine[i]);
+        const float now = fmaxf(was, ldexpf(1.f, scale_exponent(amax)));
+        uint8_t* dst = static_cast<uint8_t*>(is_k ? p.kp : p.vp) + (slice * kPage + lo % kPage) * D;
+        if (threadIdx.x == 0) *scale = now;
+        // ---- earlier tokens under the larger scale -----------------------------------
+        if (first > lo && now != was) {
+            const float ratio = was / now;  // now is a power of two
+            for (int i = my; i < first - lo; i += SL) {
+                float y[8];
+                uint8_t* row = dst + static_cast<int64_t>(i) * D;
+                decode8(lane.load(row), y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] *= ratio;
+                lane.store(row, encode8(y));
+            }
+        }
+        // ---- the new tokens: the last chunk's values are still there ------------------
+        // The inverse of a power of two is exact, so the product is the quotient; a
+        // caller's other scale divides.
+        const bool power = (__float_as_uint(now) & 0x7fffffu) == 0;
+        const float inv = 1.f / now;
+        for (int c = chunks - 1; c >= 0; --c) {
+            if (c < chunks - 1) {
+                fetch(h, c);
+                values(c);
+            }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int pos = first + c * CH + u * SL + my;
+                if (pos >= last) continue;
+                float y[8];
+                if (power) {
+                    lane.in_order(scale8(v[u], inv), y);
+                } else {
+                    lane.in_order(v[u], y);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(y[j], now);
+                }
+                // what the format cannot hold is stored as NaN, so that it shows
+                if (odd > kMaxCode * now) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        y[j] = fabsf(y[j]) <= kMaxCode ? y[j] : __int_as_float(0x7fffffff);
+                }
+                lane.store(dst + static_cast<int64_t>(pos - lo) * D, encode8(y));
+            }
+        }
+        if (chunks > 1 && h + 1 < h_end) fetch(h + 1, 0);
     }
-    for (int i = first + my; i - my < last; i += SL) {
-        float y[8];
-        row(min(i, last - 1), y);
-        divide8(y, now);
-        if (i < last) lane.store(dst + static_cast<int64_t>(i - lo) * D, encode8(y));
-    }
+}
+
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2) fa_append_fp8_kernel(const __grid_constant__ Append p) {
+    __shared__ Shared sh;
+    if (static_cast<int>(blockIdx.x) < p.unit_ctas) append_block<D, INTER>(p, blockIdx.x, sh);
+    else append_rows<D, INTER, false>(p, blockIdx.x - p.unit_ctas, sh);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -471,16 +591,24 @@ int fill(Append& p, const void* q_new, const void* k_new, const void* v_new,
     return FA_OK;
 }
 
+// Tokens of a CTA that takes rows: at most kTokens, and fewer where that would
+// leave SMs without one.
+int tokens_of(int total, int num_sms) {
+    const int t = total / (num_sms * 4);
+    return t < 1 ? 1 : t > kTokens ? kTokens : t;
+}
+
 template <int D, bool INTER>
 int launch_rope(const Append& p, cudaStream_t st) {
-    fa_append_rope_kernel<D, INTER><<<p.total, kThreads, 0, st>>>(p);
+    fa_append_rope_kernel<D, INTER>
+        <<<(p.total + p.tokens - 1) / p.tokens, kThreads, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, bool INTER>
 int launch_fp8(const Append& p, cudaStream_t st) {
-    const int64_t ctas = static_cast<int64_t>(p.units) * 2 * p.Hk + (p.q ? p.total : 0);
-    fa_append_fp8_kernel<D, INTER><<<static_cast<unsigned>(ctas), kThreads, 0, st>>>(p);
+    const int row_ctas = p.q ? (p.total + p.tokens - 1) / p.tokens : 0;
+    fa_append_fp8_kernel<D, INTER><<<p.unit_ctas + row_ctas, kThreads, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -505,6 +633,7 @@ int fa_append_paged_rope(const void* q_new, const void* k_new, const void* v_new
     int num_sms = 0;
     if (rc != FA_OK || (rc = fa::device_error_word(&p.err, &num_sms)) != FA_OK) return rc;
     if (total_new == 0) return FA_OK;
+    p.tokens = fa::tokens_of(total_new, num_sms);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (d == 64)
         return interleaved ? fa::launch_rope<64, true>(p, st) : fa::launch_rope<64, false>(p, st);
@@ -543,6 +672,11 @@ int fa_append_paged_fp8(const void* q_new, const void* k_new, const void* v_new,
     int num_sms = 0;
     if ((rc = fa::device_error_word(&p.err, &num_sms)) != FA_OK) return rc;
     if (total_new == 0) return FA_OK;
+    p.tokens = fa::tokens_of(total_new, num_sms);
+    // heads of a unit's CTA: up to 8, and fewer where SMs would be short of CTAs
+    const int64_t pairs = static_cast<int64_t>(p.units) * 2 * H_kv / (num_sms * 8);
+    p.unit_heads = static_cast<int>(pairs < 1 ? 1 : pairs > 8 ? 8 : pairs);
+    p.unit_ctas = p.units * 2 * ((H_kv + p.unit_heads - 1) / p.unit_heads);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (d == 64)
         return interleaved ? fa::launch_fp8<64, true>(p, st) : fa::launch_fp8<64, false>(p, st);

@@ -16,6 +16,12 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFwdHeads = 4;  // heads a slot takes
+constexpr int kBwdHeads = 4;
+constexpr int kFwdCtas = 32;  // CTAs per SM of the grids, at most
+// The backward grid is what is resident: 3 CTAs of 80 registers an SM, 220 us
+// for 36800 tokens of 40 heads; 2 heads a slot 238, 6 CTAs in two waves 243.
+constexpr int kBwdCtas = 3;
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 // ---------------------------------------------------------------------------
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const __grid_con
 // thread sums dw over its rows in registers, the CTA over its threads in
 // shared memory, and a second kernel over the CTAs in fp64: a fixed order.
 template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBwdCtas)
     fa_norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     __shared__ float red[SL][D];
@@ -309,11 +315,6 @@ __global__ void __launch_bounds__(D* kSumRows)
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-constexpr int kFwdHeads = 4;  // heads a slot takes
-constexpr int kBwdHeads = 2;
-constexpr int kFwdCtas = 32;  // CTAs per SM of the grids, at most
-constexpr int kBwdCtas = 3;
 
 // The rows of a tensor with `heads` heads: packed tokens `stride` apart (0:
 // back to back), or [B, heads, N, d].
