@@ -15,6 +15,7 @@
 // shared by the CTA's tokens, where a plan kernel would be a launch of its own.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "fa_internal.h"
@@ -27,7 +28,9 @@ constexpr int kPage = 256;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 16;  // of a CTA, at most, where rows are taken one by one
-constexpr int kRows = 4;     // a thread has in flight
+constexpr int kRows = 4;     // of a thread at a time
+constexpr int kStages = 4;   // 8-bit pages: chunks of new rows on their way, less one
+constexpr int kRing = kStages * kRows * kThreads * 16;  // bytes of shared memory
 
 struct Append {
     const __nv_bfloat16 *q, *k, *v;  // new rows, `stride` elements a token apart
@@ -279,11 +282,17 @@ __global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const __grid_c
 // ---------------------------------------------------------------------------
 constexpr float kMaxCode = 448.f;
 
-// The least e in [-64, 64] with a <= 448 * 2^e (448 = 0.875 * 2^9).
-__device__ __forceinline__ int scale_exponent(float a) {
-    int e;
-    const float m = frexpf(a, &e);
-    return a > 0.f ? min(max(e - 9 + (m > 0.875f), -64), 64) : -64;
+// The least power of two s in [2^-64, 2^64] with a <= 448 s, a finite.  With
+// a = m 2^E, m in [1, 2), and 448 = 1.75 * 2^8 it is 2^(E - 8), or the next one
+// where m > 1.75: a quarter less one ulp, added to the bits, carries just then.
+__device__ __forceinline__ float least_scale(float a) {
+    const int f = static_cast<int>((__float_as_uint(a) + 0x1fffffu) >> 23) - 8;
+    return __uint_as_float(static_cast<uint32_t>(min(max(f, 63), 191)) << 23);
+}
+
+// 1 / s of a power of two in that range.
+__device__ __forceinline__ float inverse_power(float s) {
+    return __uint_as_float((254u << 23) - __float_as_uint(s));
 }
 
 // 8-bit codes of values already divided by the scale: to nearest even.
@@ -386,148 +395,341 @@ __device__ __forceinline__ float largest8(const Vec8& v) {
     return max3f(m, fabsf(f2_lo(v.b[1])), fabsf(f2_hi(v.b[1])));
 }
 
+// The largest finite magnitude of a lane's rows; `odd`: infinities too.
 template <int D, bool INTER>
-__device__ __forceinline__ void append_block(const Append& p, int cta, Shared& sh) {
+__device__ __forceinline__ float finite_max(const Vec8 (&v)[kRows], float& odd) {
+    float m = 0.f;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) m = fmaxf(m, largest8(v[u]));
+    odd = m;
+    if (m == INFINITY) {  // rare: once more without them
+        m = 0.f;
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            float y[8];
+            Lane<D, INTER>::in_order(v[u], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (fabsf(y[j]) < INFINITY) m = fmaxf(m, fabsf(y[j]));
+        }
+    }
+    return m;
+}
+
+// A lane's codes of v / scale.  The inverse of a power of two is exact, so the
+// product is the quotient, and with `odd` (the lane's largest magnitude) in
+// reach of the format there is no more to it; a caller's other scale divides,
+// and what the format cannot hold is stored as NaN, so that it shows.
+template <int D, bool INTER>
+__device__ __forceinline__ uint2 codes8(const Vec8& v, float scale, float odd) {
+    float y[8];
+    const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
+    if (power && odd <= kMaxCode * scale) {
+        Lane<D, INTER>::in_order(scale8(v, inverse_power(scale)), y);
+    } else {
+        Lane<D, INTER>::in_order(v, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            y[j] = __fdiv_rn(y[j], scale);
+            if (!(fabsf(y[j]) <= kMaxCode)) y[j] = __int_as_float(0x7fffffff);
+        }
+    }
+    return encode8(y);
+}
+
+// Codes under a scale 1 / `ratio` times the old one.
+template <int D, bool INTER>
+__device__ __forceinline__ uint2 rescaled(const uint2& codes, float ratio) {
+    float y[8];
+    decode8(codes, y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] *= ratio;
+    return encode8(y);
+}
+
+// A block's `rows` earlier tokens under it, by the whole CTA.
+template <int D, bool INTER>
+__device__ __forceinline__ void rescale_rows(uint8_t* dst, int rows, float ratio,
+                                             const Lane<D, INTER>& lane) {
+    constexpr int SL = kThreads / (D / 8);
+    for (int i = threadIdx.x / (D / 8); i < rows; i += SL * kRows) {
+        uint2 c[kRows];
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+            if (i + u * SL < rows) c[u] = lane.load(dst + (i + u * SL) * D);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u)
+            if (i + u * SL < rows)
+                lane.store(dst + (i + u * SL) * D, rescaled<D, INTER>(c[u], ratio));
+    }
+}
+
+// A block with new tokens: where it is.
+struct Block {
+    int64_t slice0;            // page * heads
+    int lo, first, last, row;  // positions; the row of `first`
+    int at;                    // the block's first slot in its page
+};
+
+// 16 bytes from global into shared memory without a register; zeros where
+// `take` is false.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+                 "r"(take ? 16 : 0)
+                 : "memory");
+}
+
+template <int D, bool INTER>
+__device__ __forceinline__ void append_block(const Append& p, const Block& b, bool is_k,
+                                             int h_begin, int h_end, uint4* ring) {
     constexpr int LPR = D / 8, SL = kThreads / LPR, CH = SL * kRows;  // tokens at a time
     __shared__ float red[2][kWarps];
     const Lane<D, INTER> lane(p.t.half);
     const int my = threadIdx.x / LPR;
-    const int hgroups = (p.Hk + p.unit_heads - 1) / p.unit_heads;
-    const int unit = cta / (2 * hgroups), sub = cta - unit * 2 * hgroups;
-    const bool is_k = sub < hgroups;
-    const int h_begin = (is_k ? sub : sub - hgroups) * p.unit_heads;
-    const int h_end = min(h_begin + p.unit_heads, p.Hk);
-    Seq s;
-    int blk = 0;
-    if (!find_unit(p, unit, sh, s, blk)) return;
-    const int lg = p.block_log2, start = s.len - s.n;
-    const int lo = blk << lg;  // the block's first position
-    const int first = max(lo, start), last = min(lo + (1 << lg), s.len);
-    const int page = page_at(p, s, lo);
-    if (page < 0) return;
-    const int chunks = (last - first + CH - 1) / CH;
+    const int rows = b.last - b.first, chunks = (rows + CH - 1) / CH;
     const bool norms = is_k && p.wk.w;
     Vec8 w = {};
     if (norms) w = lane.weights(p.wk);
     Rotation<D, INTER> rot[kRows];
     int turned = -1;  // the chunk that `rot` is of
     const int64_t sx = is_k ? p.sk : p.sv;
-    const __nv_bfloat16* x0 = (is_k ? p.k : p.v) + (s.row0 + (first - start)) * sx;
-    uint4 raw[kRows];
-    auto fetch = [&](int h, int c) {
+    const __nv_bfloat16* x0 = (is_k ? p.k : p.v) + (b.row + my) * sx;
+    // A ring of chunks on their way: a slot's rows are copied, and read, by its
+    // own lanes, so that a warp waits for nothing but its own copies.
+    int ask_h = h_begin, ask_c = 0, ask_at = 0, at = 0;
+    auto ask = [&]() {
+        if (ask_h < h_end) {
+            const __nv_bfloat16* x = x0 + ask_c * CH * sx + ask_h * D + 8 * lane.chunk;
+            uint4* dst = ring + ask_at * (kRows * kThreads) + threadIdx.x;
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int r = c * CH + u * SL + my;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (first + r < last) raw[u] = lane.load(x0 + r * sx + static_cast<int64_t>(h) * D);
+            for (int u = 0; u < kRows; ++u) {
+                const bool take = ask_c * CH + u * SL + my < rows;
+                copy16(dst + u * kThreads, take ? x : p.k, take);
+                x += SL * sx;
+            }
+            if (++ask_c == chunks) {
+                ask_c = 0;
+                ++ask_h;
+            }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ask_at = ask_at + 1 == kStages ? 0 : ask_at + 1;
     };
     Vec8 v[kRows];
-    auto values = [&](int c) {  // of the rows in `raw`, normed and rotated
+    auto turn = [&](int c) {  // v's rows, of chunk c, normed and rotated
         if (is_k && turned != c) {
             turned = c;
 #pragma unroll
             for (int u = 0; u < kRows; ++u)
-                rot[u].load(p.t, min(first + c * CH + u * SL + my, last - 1), lane);
+                rot[u].load(p.t, min(b.first + c * CH + u * SL + my, b.last - 1), lane);
         }
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            v[u] = lane.unpack(raw[u]);
             if (norms) v[u] = norm_row<D>(v[u], w, p.eps);
             if (is_k) rot[u].apply(v[u]);
         }
     };
-    fetch(h_begin, 0);
-    for (int h = h_begin; h < h_end; ++h) {
-        // ---- the largest finite magnitude; `odd`: infinities too -------------------
+    auto take = [&](int c) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();
+        const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(
+            ring + at * (kRows * kThreads) + my * LPR);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const __nv_bfloat16* r = row + u * (kThreads * 8);
+            const uint2 lo = *reinterpret_cast<const uint2*>(r + lane.lo);
+            const uint2 hi = *reinterpret_cast<const uint2*>(r + lane.hi);
+            v[u] = lane.unpack(make_uint4(lo.x, lo.y, hi.x, hi.y));
+        }
+        at = at + 1 == kStages ? 0 : at + 1;
+        turn(c);
+        ask();  // into the stage read before this one
+    };
+    const int per_page = kPage >> p.block_log2;
+    float* scale = (is_k ? p.ks : p.vs) + (b.slice0 + h_begin) * per_page + (b.at >> p.block_log2);
+    uint8_t* dst = static_cast<uint8_t*>(is_k ? p.kp : p.vp) +
+                   ((b.slice0 + h_begin) * kPage + b.at) * D;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) ask();
+    for (int h = h_begin; h < h_end; ++h, scale += per_page, dst += kPage * D) {
+        const float was = b.first > b.lo ? *scale : 0.f;
         float amax = 0.f, odd = 0.f;
         for (int c = 0; c < chunks; ++c) {
-            if (c > 0) fetch(h, c);
-            values(c);
-            float m = 0.f;
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) m = fmaxf(m, largest8(v[u]));
-            odd = fmaxf(odd, m);
-            if (m == INFINITY) {  // rare: once more without them
-                m = 0.f;
-#pragma unroll
-                for (int u = 0; u < kRows; ++u) {
-                    float y[8];
-                    lane.in_order(v[u], y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (fabsf(y[j]) < INFINITY) m = fmaxf(m, fabsf(y[j]));
-                }
-            }
-            amax = fmaxf(amax, m);
+            take(c);
+            float o;
+            amax = fmaxf(amax, finite_max<D, INTER>(v, o));
+            odd = fmaxf(odd, o);
         }
-        if (chunks == 1 && h + 1 < h_end) fetch(h + 1, 0);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // (bits of non-negative floats are in their order)
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
         float* mine = red[h & 1];  // two, so that one barrier a head will do
-        if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = amax;
-        const int64_t slice = static_cast<int64_t>(page) * p.Hk + h;
-        float* scale = (is_k ? p.ks : p.vs) + slice * (kPage >> lg) + ((lo % kPage) >> lg);
-        const float was = first > lo ? *scale : 0.f;
+        if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = __uint_as_float(top);
         __syncthreads();  // every thread has read the old scale
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) amax = fmaxf(amax, mine[i]);
-        const float now = fmaxf(was, ldexpf(1.f, scale_exponent(amax)));
-        uint8_t* dst = static_cast<uint8_t*>(is_k ? p.kp : p.vp) + (slice * kPage + lo % kPage) * D;
+        const float now = fmaxf(was, least_scale(amax));
         if (threadIdx.x == 0) *scale = now;
-        // ---- earlier tokens under the larger scale -----------------------------------
-        if (first > lo && now != was) {
-            const float ratio = was / now;  // now is a power of two
-            for (int i = my; i < first - lo; i += SL) {
-                float y[8];
-                uint8_t* row = dst + static_cast<int64_t>(i) * D;
-                decode8(lane.load(row), y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] *= ratio;
-                lane.store(row, encode8(y));
-            }
-        }
-        // ---- the new tokens: the last chunk's values are still there ------------------
-        // The inverse of a power of two is exact, so the product is the quotient; a
-        // caller's other scale divides.
-        const bool power = (__float_as_uint(now) & 0x7fffffu) == 0;
-        const float inv = 1.f / now;
+        if (b.first > b.lo && now != was)  // now is a power of two
+            rescale_rows<D, INTER>(dst, b.first - b.lo, was * inverse_power(now), lane);
+        // the new tokens: the last chunk's values are still there
         for (int c = chunks - 1; c >= 0; --c) {
             if (c < chunks - 1) {
-                fetch(h, c);
-                values(c);
+                const __nv_bfloat16* x = x0 + c * CH * sx + h * D;
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) {  // (only the last chunk has rows missing)
+                    v[u] = lane.unpack(lane.load(x));
+                    x += SL * sx;
+                }
+                turn(c);
             }
+            uint8_t* row = dst + (b.first - b.lo + c * CH + my) * D;
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
-                const int pos = first + c * CH + u * SL + my;
-                if (pos >= last) continue;
-                float y[8];
-                if (power) {
-                    lane.in_order(scale8(v[u], inv), y);
-                } else {
-                    lane.in_order(v[u], y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(y[j], now);
-                }
-                // what the format cannot hold is stored as NaN, so that it shows
-                if (odd > kMaxCode * now) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        y[j] = fabsf(y[j]) <= kMaxCode ? y[j] : __int_as_float(0x7fffffff);
-                }
-                lane.store(dst + static_cast<int64_t>(pos - lo) * D, encode8(y));
+                if (c * CH + u * SL + my < rows)
+                    lane.store(row, codes8<D, INTER>(v[u], now, odd));
+                row += SL * D;
             }
         }
-        if (chunks > 1 && h + 1 < h_end) fetch(h + 1, 0);
     }
 }
 
+// A block where sequences have a few new tokens each, as in a decode step: each
+// slot takes one head of K or of V (pairs pair_begin .. pair_end - 1, the keys
+// first), kRows tokens at a time, and finds its scale alone; where scales grow,
+// the CTA rounds the earlier tokens of those heads together.
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) fa_append_fp8_kernel(const __grid_constant__ Append p) {
+__device__ __forceinline__ void append_few(const Append& p, const Block& b, int pair_begin,
+                                           int pair_end) {
+    constexpr int LPR = D / 8, SL = kThreads / LPR;
+    __shared__ float ratio[SL];  // of each slot's head; 0: nothing to round again
+    const Lane<D, INTER> lane(p.t.half);
+    const int my = threadIdx.x / LPR;
+    const int rows = b.last - b.first, chunks = (rows + kRows - 1) / kRows;
+    const int per_page = kPage >> p.block_log2;
+    Vec8 w = {};
+    if (p.wk.w) w = lane.weights(p.wk);
+    for (int base = pair_begin; base < pair_end; base += SL) {
+        const bool live = base + my < pair_end;
+        const int pair = live ? base + my : pair_end - 1;
+        const bool is_k = pair < p.Hk;
+        const int h = is_k ? pair : pair - p.Hk;
+        const int64_t sx = is_k ? p.sk : p.sv;
+        const __nv_bfloat16* x = (is_k ? p.k : p.v) + b.row * sx + h * D;
+        float* scale = (is_k ? p.ks : p.vs) + (b.slice0 + h) * per_page + (b.at >> p.block_log2);
+        float was = 0.f;
+        if (b.first > b.lo && lane.chunk == 0) was = *scale;
+        was = __shfl_sync(0xffffffffu, was, threadIdx.x & 31 & ~(LPR - 1));
+        Vec8 v[kRows];
+        auto take = [&](int c) {
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int r = c * kRows + u;
+                v[u] = lane.unpack(r < rows ? lane.load(x + r * sx) : make_uint4(0, 0, 0, 0));
+            }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                if (p.wk.w) {  // a warp's slots may be of keys and of values
+                    const Vec8 n = norm_row<D>(v[u], w, p.eps);
+                    if (is_k) v[u] = n;
+                }
+                Rotation<D, INTER> rot;
+                rot.load(p.t, min(b.first + c * kRows + u, b.last - 1), lane);
+                if (is_k) rot.apply(v[u]);
+            }
+        };
+        float amax = 0.f, odd = 0.f;
+        for (int c = 0; c < chunks; ++c) {
+            take(c);
+            float o;
+            amax = fmaxf(amax, finite_max<D, INTER>(v, o));
+            odd = fmaxf(odd, o);
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float now = fmaxf(was, least_scale(amax));
+        uint8_t* dst = static_cast<uint8_t*>(is_k ? p.kp : p.vp) +
+                       ((b.slice0 + h) * kPage + b.at) * D;
+        if (live && lane.chunk == 0) *scale = now;
+        for (int c = chunks - 1; c >= 0; --c) {
+            if (c < chunks - 1) take(c);
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int r = c * kRows + u;
+                if (live && r < rows)
+                    lane.store(dst + (b.first - b.lo + r) * D, codes8<D, INTER>(v[u], now, odd));
+            }
+        }
+        if (b.first == b.lo) continue;  // the same for the CTA
+        if (lane.chunk == 0) ratio[my] = live && now != was ? was * inverse_power(now) : 0.f;
+        __syncthreads();
+        // rows of all the slots' heads, kFew of them in flight for each slot
+        constexpr int kFew = 8;
+        const int old = b.first - b.lo, all = min(SL, pair_end - base) * old;
+        for (int i = my; i < all; i += SL * kFew) {
+            uint8_t* row[kFew];
+            uint2 c[kFew];
+            float f[kFew];
+#pragma unroll
+            for (int u = 0; u < kFew; ++u) {
+                const int at = i + u * SL, slot = at / old;
+                f[u] = at < all ? ratio[slot] : 0.f;
+                if (f[u] == 0.f) continue;
+                const int pr = base + slot, hh = pr < p.Hk ? pr : pr - p.Hk;
+                row[u] = static_cast<uint8_t*>(pr < p.Hk ? p.kp : p.vp) +
+                         ((b.slice0 + hh) * kPage + b.at + at - slot * old) * D;
+                c[u] = lane.load(row[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kFew; ++u)
+                if (f[u] != 0.f) lane.store(row[u], rescaled<D, INTER>(c[u], f[u]));
+        }
+        __syncthreads();
+    }
+}
+
+// The block of unit `unit`; false: none, or none that can be taken.
+__device__ __forceinline__ bool find_block(const Append& p, int unit, Shared& sh, Block& b) {
+    Seq s;
+    int blk = 0;
+    if (!find_unit(p, unit, sh, s, blk)) return false;
+    const int start = s.len - s.n;
+    b.lo = blk << p.block_log2;
+    b.first = max(b.lo, start);
+    b.last = min(b.lo + (1 << p.block_log2), s.len);
+    b.row = s.row0 + (b.first - start);
+    b.at = b.lo % kPage;
+    const int page = page_at(p, s, b.lo);
+    b.slice0 = static_cast<int64_t>(page) * p.Hk;
+    return page >= 0;
+}
+
+// The first CTAs take units, unit_ctas of them: for each unit as many as
+// cover the heads of K and then those of V, unit_heads each (FEW: the heads of
+// both together).  The others take the queries' rows.
+template <int D, bool INTER, bool FEW>
+__global__ void __launch_bounds__(kThreads, 2)
+    fa_append_fp8_kernel(const __grid_constant__ Append p) {
     __shared__ Shared sh;
-    if (static_cast<int>(blockIdx.x) < p.unit_ctas) append_block<D, INTER>(p, blockIdx.x, sh);
-    else append_rows<D, INTER, false>(p, blockIdx.x - p.unit_ctas, sh);
+    extern __shared__ uint4 ring[];
+    const int cta = blockIdx.x;
+    if (cta >= p.unit_ctas) {
+        append_rows<D, INTER, false>(p, cta - p.unit_ctas, sh);
+        return;
+    }
+    const int hgroups = (p.Hk + p.unit_heads - 1) / p.unit_heads;
+    const int per_unit = FEW ? (2 * p.Hk + p.unit_heads - 1) / p.unit_heads : 2 * hgroups;
+    const int unit = cta / per_unit, sub = cta - unit * per_unit;
+    Block b;
+    if (!find_block(p, unit, sh, b)) return;
+    if constexpr (FEW) {
+        const int first = sub * p.unit_heads;
+        append_few<D, INTER>(p, b, first, min(first + p.unit_heads, 2 * p.Hk));
+    } else {
+        const bool is_k = sub < hgroups;
+        const int first = (is_k ? sub : sub - hgroups) * p.unit_heads;
+        append_block<D, INTER>(p, b, is_k, first, min(first + p.unit_heads, p.Hk), ring);
+    }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -606,9 +808,27 @@ int launch_rope(const Append& p, cudaStream_t st) {
 }
 
 template <int D, bool INTER>
-int launch_fp8(const Append& p, cudaStream_t st) {
-    const int row_ctas = p.q ? (p.total + p.tokens - 1) / p.tokens : 0;
-    fa_append_fp8_kernel<D, INTER><<<p.unit_ctas + row_ctas, kThreads, 0, st>>>(p);
+int launch_fp8(Append& p, int num_sms, cudaStream_t st) {
+    // Sequences with a few tokens each: a slot takes a head, and as many heads go
+    // to a CTA as make two CTAs an SM.  Else up to 16 heads of a unit one after
+    // the other, and fewer where SMs would be short of CTAs.
+    const int64_t heads = static_cast<int64_t>(p.units) * 2 * p.Hk;
+    const bool few = p.total <= static_cast<int64_t>(p.B) * kRows;
+    int64_t each = few ? (heads + num_sms * 2 - 1) / (num_sms * 2) : heads / (num_sms * 3);
+    each = std::min<int64_t>(std::max<int64_t>(each, 1), std::min(16, few ? 2 * p.Hk : p.Hk));
+    p.unit_heads = static_cast<int>(each);
+    p.unit_ctas = p.units * static_cast<int>(few ? (2 * p.Hk + each - 1) / each
+                                                 : 2 * ((p.Hk + each - 1) / each));
+    const int ctas = p.unit_ctas + (p.q ? (p.total + p.tokens - 1) / p.tokens : 0);
+    if (few) {
+        fa_append_fp8_kernel<D, INTER, true><<<ctas, kThreads, 0, st>>>(p);
+    } else {
+        auto kernel = fa_append_fp8_kernel<D, INTER, false>;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing) !=
+            cudaSuccess)
+            return FA_ERR_CUDA;
+        kernel<<<ctas, kThreads, kRing, st>>>(p);
+    }
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -673,14 +893,12 @@ int fa_append_paged_fp8(const void* q_new, const void* k_new, const void* v_new,
     if ((rc = fa::device_error_word(&p.err, &num_sms)) != FA_OK) return rc;
     if (total_new == 0) return FA_OK;
     p.tokens = fa::tokens_of(total_new, num_sms);
-    // heads of a unit's CTA: up to 8, and fewer where SMs would be short of CTAs
-    const int64_t pairs = static_cast<int64_t>(p.units) * 2 * H_kv / (num_sms * 8);
-    p.unit_heads = static_cast<int>(pairs < 1 ? 1 : pairs > 8 ? 8 : pairs);
-    p.unit_ctas = p.units * 2 * ((H_kv + p.unit_heads - 1) / p.unit_heads);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (d == 64)
-        return interleaved ? fa::launch_fp8<64, true>(p, st) : fa::launch_fp8<64, false>(p, st);
-    return interleaved ? fa::launch_fp8<128, true>(p, st) : fa::launch_fp8<128, false>(p, st);
+        return interleaved ? fa::launch_fp8<64, true>(p, num_sms, st)
+                           : fa::launch_fp8<64, false>(p, num_sms, st);
+    return interleaved ? fa::launch_fp8<128, true>(p, num_sms, st)
+                       : fa::launch_fp8<128, false>(p, num_sms, st);
 }
 
 }  // extern "C"
