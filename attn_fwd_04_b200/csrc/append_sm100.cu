@@ -395,17 +395,17 @@ __device__ __forceinline__ float largest8(const Vec8& v) {
     return max3f(m, fabsf(f2_lo(v.b[1])), fabsf(f2_hi(v.b[1])));
 }
 
-// The largest finite magnitude of a lane's rows; `odd`: infinities too.
-template <int D, bool INTER>
-__device__ __forceinline__ float finite_max(const Vec8 (&v)[kRows], float& odd) {
+// The largest finite magnitude of R of a lane's rows; `odd`: infinities too.
+template <int D, bool INTER, int R>
+__device__ __forceinline__ float finite_max(const Vec8* v, float& odd) {
     float m = 0.f;
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) m = fmaxf(m, largest8(v[u]));
+    for (int u = 0; u < R; ++u) m = fmaxf(m, largest8(v[u]));
     odd = m;
     if (m == INFINITY) {  // rare: once more without them
         m = 0.f;
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
+        for (int u = 0; u < R; ++u) {
             float y[8];
             Lane<D, INTER>::in_order(v[u], y);
 #pragma unroll
@@ -417,14 +417,17 @@ __device__ __forceinline__ float finite_max(const Vec8 (&v)[kRows], float& odd) 
 }
 
 // A lane's codes of v / scale.  The inverse of a power of two is exact, so the
-// product is the quotient, and with `odd` (the lane's largest magnitude) in
-// reach of the format there is no more to it; a caller's other scale divides,
-// and what the format cannot hold is stored as NaN, so that it shows.
+// product is the quotient, and where the lane's largest magnitude `odd` is in
+// reach of the format there is no more to it (`simple`); a caller's other scale
+// divides, and what the format cannot hold is stored as NaN, so that it shows.
+__device__ __forceinline__ bool simple_scale(float scale, float odd) {
+    return (__float_as_uint(scale) & 0x7fffffu) == 0 && odd <= kMaxCode * scale;
+}
+
 template <int D, bool INTER>
-__device__ __forceinline__ uint2 codes8(const Vec8& v, float scale, float odd) {
+__device__ __forceinline__ uint2 codes8(const Vec8& v, float scale, bool simple) {
     float y[8];
-    const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
-    if (power && odd <= kMaxCode * scale) {
+    if (simple) {
         Lane<D, INTER>::in_order(scale8(v, inverse_power(scale)), y);
     } else {
         Lane<D, INTER>::in_order(v, y);
@@ -447,20 +450,20 @@ __device__ __forceinline__ uint2 rescaled(const uint2& codes, float ratio) {
     return encode8(y);
 }
 
-// A block's `rows` earlier tokens under it, by the whole CTA.
+// A block's `rows` earlier tokens under it, by `slots` slots, of which this is
+// number `slot`.
 template <int D, bool INTER>
-__device__ __forceinline__ void rescale_rows(uint8_t* dst, int rows, float ratio,
-                                             const Lane<D, INTER>& lane) {
-    constexpr int SL = kThreads / (D / 8);
-    for (int i = threadIdx.x / (D / 8); i < rows; i += SL * kRows) {
+__device__ __forceinline__ void rescale_rows(uint8_t* dst, int rows, float ratio, int slot,
+                                             int slots, const Lane<D, INTER>& lane) {
+    for (int i = slot; i < rows; i += slots * kRows) {
         uint2 c[kRows];
 #pragma unroll
         for (int u = 0; u < kRows; ++u)
-            if (i + u * SL < rows) c[u] = lane.load(dst + (i + u * SL) * D);
+            if (i + u * slots < rows) c[u] = lane.load(dst + (i + u * slots) * D);
 #pragma unroll
         for (int u = 0; u < kRows; ++u)
-            if (i + u * SL < rows)
-                lane.store(dst + (i + u * SL) * D, rescaled<D, INTER>(c[u], ratio));
+            if (i + u * slots < rows)
+                lane.store(dst + (i + u * slots) * D, rescaled<D, INTER>(c[u], ratio));
     }
 }
 
@@ -479,21 +482,32 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool take) {
                  : "memory");
 }
 
-template <int D, bool INTER>
+// The CTA's slots times kRows are CH rows: a head's CH tokens at a time (larger
+// blocks in chunks), or the block's tokens of CH / block heads at once.  A
+// thread's rows are of kRows / UH heads, UH rows each, UH = block / slots; where
+// a block has fewer tokens than there are slots (16 tokens of 64 values), the
+// first half of the CTA's warps and the second take heads of their own.
+template <int D, bool INTER, int UH>
 __device__ __forceinline__ void append_block(const Append& p, const Block& b, bool is_k,
                                              int h_begin, int h_end, uint4* ring) {
-    constexpr int LPR = D / 8, SL = kThreads / LPR, CH = SL * kRows;  // tokens at a time
-    __shared__ float red[2][kWarps];
+    constexpr int LPR = D / 8, SL = kThreads / LPR, CH = SL * kRows, NH = kRows / UH;
+    __shared__ float red[2][NH][kWarps];
     const Lane<D, INTER> lane(p.t.half);
+    const int block = 1 << p.block_log2;
     const int my = threadIdx.x / LPR;
-    const int rows = b.last - b.first, chunks = (rows + CH - 1) / CH;
+    const int parts = UH == 1 && block < SL ? SL / block : 1;  // of the CTA, with heads of their own
+    const int part = parts > 1 ? my / block : 0, tok = parts > 1 ? my % block : my;
+    const int at_once = NH * parts;  // heads
+    const int rows = b.last - b.first, chunks = UH == kRows ? (rows + CH - 1) / CH : 1;
     const bool norms = is_k && p.wk.w;
     Vec8 w = {};
     if (norms) w = lane.weights(p.wk);
-    Rotation<D, INTER> rot[kRows];
+    Rotation<D, INTER> rot[UH];
     int turned = -1;  // the chunk that `rot` is of
     const int64_t sx = is_k ? p.sk : p.sv;
-    const __nv_bfloat16* x0 = (is_k ? p.k : p.v) + (b.row + my) * sx;
+    const __nv_bfloat16* x0 = (is_k ? p.k : p.v) + (b.row + tok) * sx + part * D;
+    // row u of this thread: token tok + (u % UH) * SL of the chunk, head h + part
+    // + (u / UH) * parts
     // A ring of chunks on their way: a slot's rows are copied, and read, by its
     // own lanes, so that a warp waits for nothing but its own copies.
     int ask_h = h_begin, ask_c = 0, ask_at = 0, at = 0;
@@ -503,13 +517,14 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
             uint4* dst = ring + ask_at * (kRows * kThreads) + threadIdx.x;
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
-                const bool take = ask_c * CH + u * SL + my < rows;
-                copy16(dst + u * kThreads, take ? x : p.k, take);
-                x += SL * sx;
+                const bool take = ask_c * CH + (u % UH) * SL + tok < rows &&
+                                  ask_h + part + (u / UH) * parts < h_end;
+                copy16(dst + u * kThreads,
+                       take ? x + (u % UH) * SL * sx + (u / UH) * parts * D : p.k, take);
             }
             if (++ask_c == chunks) {
                 ask_c = 0;
-                ++ask_h;
+                ask_h += at_once;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -517,16 +532,20 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
     };
     Vec8 v[kRows];
     auto turn = [&](int c) {  // v's rows, of chunk c, normed and rotated
-        if (is_k && turned != c) {
+        if (norms) {
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) v[u] = norm_row<D>(v[u], w, p.eps);
+        }
+        if (!is_k) return;
+        if (turned != c) {
             turned = c;
 #pragma unroll
-            for (int u = 0; u < kRows; ++u)
-                rot[u].load(p.t, min(b.first + c * CH + u * SL + my, b.last - 1), lane);
+            for (int u = 0; u < UH; ++u)
+                rot[u].load(p.t, min(b.first + c * CH + u * SL + tok, b.last - 1), lane);
         }
+        if (lane.turns) {
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            if (norms) v[u] = norm_row<D>(v[u], w, p.eps);
-            if (is_k) rot[u].apply(v[u]);
+            for (int u = 0; u < kRows; ++u) rot[u % UH].turn(v[u]);
         }
     };
     auto take = [&](int c) {
@@ -546,31 +565,48 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
         ask();  // into the stage read before this one
     };
     const int per_page = kPage >> p.block_log2;
-    float* scale = (is_k ? p.ks : p.vs) + (b.slice0 + h_begin) * per_page + (b.at >> p.block_log2);
-    uint8_t* dst = static_cast<uint8_t*>(is_k ? p.kp : p.vp) +
-                   ((b.slice0 + h_begin) * kPage + b.at) * D;
+    float* scales = (is_k ? p.ks : p.vs) + b.slice0 * per_page + (b.at >> p.block_log2);
+    uint8_t* codes = static_cast<uint8_t*>(is_k ? p.kp : p.vp) + (b.slice0 * kPage + b.at) * D;
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) ask();
-    for (int h = h_begin; h < h_end; ++h, scale += per_page, dst += kPage * D) {
-        const float was = b.first > b.lo ? *scale : 0.f;
-        float amax = 0.f, odd = 0.f;
+    for (int h = h_begin; h < h_end; h += at_once) {
+        float was[NH], amax[NH], odd[NH];
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const int head = h + part + n * parts;
+            was[n] = b.first > b.lo && head < h_end ? scales[head * per_page] : 0.f;
+            amax[n] = odd[n] = 0.f;
+        }
         for (int c = 0; c < chunks; ++c) {
             take(c);
-            float o;
-            amax = fmaxf(amax, finite_max<D, INTER>(v, o));
-            odd = fmaxf(odd, o);
-        }
-        // (bits of non-negative floats are in their order)
-        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-        float* mine = red[h & 1];  // two, so that one barrier a head will do
-        if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = __uint_as_float(top);
-        __syncthreads();  // every thread has read the old scale
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) amax = fmaxf(amax, mine[i]);
-        const float now = fmaxf(was, least_scale(amax));
-        if (threadIdx.x == 0) *scale = now;
-        if (b.first > b.lo && now != was)  // now is a power of two
-            rescale_rows<D, INTER>(dst, b.first - b.lo, was * inverse_power(now), lane);
+            for (int n = 0; n < NH; ++n) {
+                float o;
+                amax[n] = fmaxf(amax[n], finite_max<D, INTER, UH>(v + n * UH, o));
+                odd[n] = fmaxf(odd[n], o);
+            }
+        }
+        float(&mine)[NH][kWarps] = red[(h - h_begin) / at_once & 1];  // two: one barrier will do
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            // (bits of non-negative floats are in their order)
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax[n]));
+            if ((threadIdx.x & 31) == 0) mine[n][threadIdx.x >> 5] = __uint_as_float(top);
+        }
+        __syncthreads();  // every thread has read the old scales
+        const int warps = kWarps / parts;
+#pragma unroll
+        for (int n = 0; n < NH; ++n) {
+            const int head = h + part + n * parts;
+            for (int i = 0; i < warps; ++i) amax[n] = fmaxf(amax[n], mine[n][part * warps + i]);
+            const float now = fmaxf(was[n], least_scale(amax[n]));
+            if (head < h_end && tok == 0 && lane.chunk == 0) scales[head * per_page] = now;
+            amax[n] = now;  // the scale from here on
+            if (b.first > b.lo && head < h_end && now != was[n])  // now is a power of two
+                rescale_rows<D, INTER>(codes + static_cast<int64_t>(head) * (kPage * D),
+                                       b.first - b.lo, was[n] * inverse_power(now), tok,
+                                       SL / parts, lane);
+        }
         // the new tokens: the last chunk's values are still there
         for (int c = chunks - 1; c >= 0; --c) {
             if (c < chunks - 1) {
@@ -582,13 +618,25 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
                 }
                 turn(c);
             }
-            uint8_t* row = dst + (b.first - b.lo + c * CH + my) * D;
+            bool simple = true;
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                if (c * CH + u * SL + my < rows)
-                    lane.store(row, codes8<D, INTER>(v[u], now, odd));
-                row += SL * D;
+            for (int n = 0; n < NH; ++n) simple = simple && simple_scale(amax[n], odd[n]);
+            uint2 out[kRows];
+            if (simple) {
+#pragma unroll
+                for (int u = 0; u < kRows; ++u) out[u] = codes8<D, INTER>(v[u], amax[u / UH], true);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kRows; ++u)
+                    out[u] = codes8<D, INTER>(v[u], amax[u / UH],
+                                              simple_scale(amax[u / UH], odd[u / UH]));
             }
+            uint8_t* dst = codes + static_cast<int64_t>(h + part) * (kPage * D) +
+                           (b.first - b.lo + c * CH + tok) * D;
+#pragma unroll
+            for (int u = 0; u < kRows; ++u)
+                if (c * CH + (u % UH) * SL + tok < rows && h + part + (u / UH) * parts < h_end)
+                    lane.store(dst + (u % UH) * SL * D + (u / UH) * parts * (kPage * D), out[u]);
         }
     }
 }
@@ -641,7 +689,7 @@ __device__ __forceinline__ void append_few(const Append& p, const Block& b, int 
         for (int c = 0; c < chunks; ++c) {
             take(c);
             float o;
-            amax = fmaxf(amax, finite_max<D, INTER>(v, o));
+            amax = fmaxf(amax, finite_max<D, INTER, kRows>(v, o));
             odd = fmaxf(odd, o);
         }
 #pragma unroll
@@ -657,7 +705,7 @@ __device__ __forceinline__ void append_few(const Append& p, const Block& b, int 
             for (int u = 0; u < kRows; ++u) {
                 const int r = c * kRows + u;
                 if (live && r < rows)
-                    lane.store(dst + (b.first - b.lo + r) * D, codes8<D, INTER>(v[u], now, odd));
+                    lane.store(dst + (b.first - b.lo + r) * D, codes8<D, INTER>(v[u], now, simple_scale(now, odd)));
             }
         }
         if (b.first == b.lo) continue;  // the same for the CTA
@@ -728,7 +776,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else {
         const bool is_k = sub < hgroups;
         const int first = (is_k ? sub : sub - hgroups) * p.unit_heads;
-        append_block<D, INTER>(p, b, is_k, first, min(first + p.unit_heads, p.Hk), ring);
+        const int end = min(first + p.unit_heads, p.Hk);
+        constexpr int SL = kThreads / (D / 8);
+        const int block = 1 << p.block_log2;
+        if (block <= SL) append_block<D, INTER, 1>(p, b, is_k, first, end, ring);
+        else if (block == 2 * SL) append_block<D, INTER, 2>(p, b, is_k, first, end, ring);
+        else append_block<D, INTER, 4>(p, b, is_k, first, end, ring);
     }
 }
 
@@ -815,7 +868,10 @@ int launch_fp8(Append& p, int num_sms, cudaStream_t st) {
     const int64_t heads = static_cast<int64_t>(p.units) * 2 * p.Hk;
     const bool few = p.total <= static_cast<int64_t>(p.B) * kRows;
     int64_t each = few ? (heads + num_sms * 2 - 1) / (num_sms * 2) : heads / (num_sms * 3);
-    each = std::min<int64_t>(std::max<int64_t>(each, 1), std::min(16, few ? 2 * p.Hk : p.Hk));
+    // (a CTA takes 64 rows of 128 values, or 128 of 64, at once)
+    const int at_once = few ? 1 : std::max(1, kThreads * kRows * 8 / D >> p.block_log2);
+    each = std::min<int64_t>(std::max<int64_t>(each, 1), 16);
+    each = std::min<int64_t>((each + at_once - 1) / at_once * at_once, few ? 2 * p.Hk : p.Hk);
     p.unit_heads = static_cast<int>(each);
     p.unit_ctas = p.units * static_cast<int>(few ? (2 * p.Hk + each - 1) / each
                                                  : 2 * ((p.Hk + each - 1) / each));

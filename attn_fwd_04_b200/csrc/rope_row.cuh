@@ -195,7 +195,10 @@ struct Rotation {
     }
 
     __device__ __forceinline__ void apply(Vec8& y) const {
-        if (!on) return;
+        if (on) turn(y);
+    }
+    // (of a lane that `on` holds for)
+    __device__ __forceinline__ void turn(Vec8& y) const {
         const uint64_t minus = f2_pack(-1.f, -1.f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
