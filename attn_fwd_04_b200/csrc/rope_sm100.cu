@@ -151,7 +151,7 @@ struct Slot {
 // The grid's first CTAs take the queries, the others the keys, each in equal
 // strides over its slots: a CTA's weights stay in registers.
 template <int D, bool INTER, int U>
-__global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const __grid_constant__ NormRope p) {
+__global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const __grid_constant__ NormRope p) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     const Lane<D, INTER> lane(p.t.half);
     const bool is_q = static_cast<int>(blockIdx.x) < p.q.ctas;
@@ -181,12 +181,20 @@ __global__ void __launch_bounds__(kThreads) fa_norm_rope_kernel(const __grid_con
         Rotation<D, INTER> rot;
         rot.load(p.t, pos, lane);
         __nv_bfloat16* y = s.y + s.ry.at(at.b, at.n, at.h0);
+        Vec8 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = lane.unpack(raw[u]);
+        if (norms) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = norm_row<D>(v[u], w, p.eps);
+        }
+        if (lane.turns) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) rot.turn(v[u]);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            Vec8 v = lane.unpack(raw[u]);
-            if (norms) v = norm_row<D>(v, w, p.eps);
-            rot.apply(v);
-            if (live && u < count) lane.store(y, bad ? make_uint4(0, 0, 0, 0) : lane.pack(v));
+            if (live && u < count) lane.store(y, bad ? make_uint4(0, 0, 0, 0) : lane.pack(v[u]));
             y += s.ry.head;
         }
     }
