@@ -1,4 +1,5 @@
-"""Build libfa.so (the CUDA library behind include/fa.h) in-tree, for sm_100a.
+"""Build libfa.so (the CUDA library behind include/fa.h) in-tree, for sm_100a, and
+_calls.so (the binding's short way into it, host code only).
 
     python -m attn_fwd_04_b200.build [--force] [--verbose]
 
@@ -9,12 +10,14 @@ FA_ERR_CUDA); the driver's tensor-map encoder is looked up at run time.
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa.so")
+CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["api.cu", "fwd_sm100.cu", "bwd_sm100.cu", "decode_sm100.cu", "decode_noalloc.cu",
            "rope_sm100.cu", "append_sm100.cu", "decode_fp8_sm100.cu"]
 HEADERS = ["fa_ptx.cuh", "fa_internal.h", "rope_row.cuh"]
@@ -33,17 +36,39 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _stale(out: str, deps) -> bool:
+    if not os.path.exists(out):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "fa.h"),
-                                                                 os.path.abspath(__file__)]
+    t = os.path.getmtime(out)
+    deps = [*deps, os.path.join(INCLUDE, "fa.h"), os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _build_calls(force: bool, verbose: bool) -> None:
+    """_calls.so, against the headers and libraries of the torch that runs this."""
+    src = os.path.join(CSRC, "calls.cpp")
+    if not force and not _stale(CALLS, [src]):
+        return
+    import torch
+    root = os.path.dirname(torch.__file__)
+    headers = [os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include"),
+               sysconfig.get_paths()["include"]]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    for h in headers:
+        cmd += ["-isystem", h]
+    cmd += [src, "-o", CALLS, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
+            "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    _build_calls(force, verbose)
+    if not force and not _stale(LIB, [os.path.join(CSRC, f) for f in SOURCES + HEADERS]):
         return LIB
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)

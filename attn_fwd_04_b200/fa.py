@@ -590,6 +590,37 @@ _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "turns": 3, "yarn": 4}
 _FP8 = torch.float8_e4m3fn
 
 
+# What _calls.so (csrc/calls.cpp) binds, in its order.
+_SHORT = ("fa_rope_table", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+          "fa_qk_norm_rope_bwd_workspace", "fa_append_paged_rope", "fa_append_paged_fp8",
+          "fa_decode_paged_fp8", "fa_decode_paged_fp8_workspace")
+_short_calls = None
+
+
+def _short():
+    """The short way into these calls: checks, outputs and scratch in C++, for
+    the ordinary case (contiguous tensors of the current GPU, its current
+    stream).  It answers None for any other, and the wrapper goes on by itself."""
+    global _short_calls
+    if _short_calls is None:
+        L = lib()
+        try:
+            from . import _calls
+        except ImportError as e:
+            raise ImportError("the binding's _calls.so is missing or of another torch; build "
+                              "it with `python -m attn_fwd_04_b200.build`") from e
+        _calls.bind(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _SHORT))
+        _short_calls = _calls
+    return _short_calls
+
+
+def _answer(out, name: str):
+    """A short call's outputs, or the error of the status it stands for."""
+    if out.__class__ is tuple:
+        return out
+    raise FaError(out, name)
+
+
 # The current stream of a GPU as a handle, without a Stream object around it
 # (1.2 us of a call that may take 10).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -676,14 +707,14 @@ def _token_rows(t, name: str, dev=None, shape=None) -> int:
         raise ValueError(f"{name} is on {t.device}, the call's inputs on GPU {dev}")
     tokens, heads, d = mine
     st, sh, sd = t.stride()
-    if sd == 1 and sh == d and st >= heads * d and st % 8 == 0:
+    if sd == 1 and sh == d and heads * d <= st < 1 << 31 and st % 8 == 0:
         return st
     if (sd != 1 and d > 1) or (sh != d and heads > 1):
         raise ValueError(f"{name}: the [heads, d] part of a token must be contiguous")
     if tokens <= 1:
         return heads * d
     raise ValueError(f"{name}: tokens must be a multiple of 8 elements apart, without "
-                     f"overlap; got a stride of {st}")
+                     f"overlap and less than 2^31; got a stride of {st}")
 
 
 def _norm_weights(q_weight, k_weight, d: int, dev: int) -> int:
@@ -723,6 +754,11 @@ def fa_rope_table(max_pos: int, rotary_dim: int, base: float = 10000.0, scaling:
     scaled for long contexts: "none", "linear", "ntk", "turns" (blended by the
     turns within original_len, between low and high) or "yarn" (a ramp over the
     pairs between them)."""
+    if rope_cos is None and rope_sin is None and device is None and stream is None:
+        out = _short().rope_table(max_pos, rotary_dim, base, _SCALINGS.get(scaling), factor,
+                                  original_len, low, high, mscale)
+        if out is not None:
+            return _answer(out, "fa_rope_table")
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
     shape = (int(max_pos), int(rotary_dim) // 2)
@@ -792,6 +828,11 @@ def fa_qk_norm_rope(q, k, q_weight=None, k_weight=None, rope_cos=None, rope_sin=
     [tokens,H_kv,d] bf16, tokens any stride apart, positions [tokens] int32; or
     [B,H,N,d] and [B,H_kv,N,d] contiguous, positions [B,N].  No positions:
     token n is at position n.  The outputs may be the inputs."""
+    if stream is None:
+        out = _short().norm(q, k, q_weight, k_weight, rope_cos, rope_sin, positions, eps,
+                            interleaved, q_out, k_out)
+        if out is not None:
+            return _answer(out, "fa_qk_norm_rope")
     dev, layout, B, N, H, H_kv, d, q_st, k_st = _qk_rows(q, k, positions)
     wt = _norm_weights(q_weight, k_weight, d, dev)
     max_pos, rot = _rope(rope_cos, rope_sin, dev)
@@ -821,6 +862,11 @@ def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope
     """Gradients of fa_qk_norm_rope: (dq, dk, dq_weight, dk_weight) from its
     inputs and its outputs' gradients; the weights' gradients are fp32 [d], None
     where there is no weight."""
+    if stream is None:
+        out = _short().norm_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope_cos, rope_sin,
+                                positions, eps, interleaved, dq, dk, dq_weight, dk_weight)
+        if out is not None:
+            return _answer(out, "fa_qk_norm_rope_bwd")
     dev, layout, B, N, H, H_kv, d, q_st, k_st = _qk_rows(q, k, positions)
     wt = _norm_weights(q_weight, k_weight, d, dev)
     max_pos, rot = _rope(rope_cos, rope_sin, dev)
@@ -901,6 +947,12 @@ def _scale_block(k_scales, v_scales, P: int, H_kv: int, page_size: int, dev: int
 def _append(name, q_new, k_new, v_new, cu_new, k_pages, v_pages, scales, page_table, seq_lens,
             rope_cos, rope_sin, q_weight, k_weight, eps, interleaved, page_size, q_out, stream):
     """Checks and call of both appends; `scales`: (k_scales, v_scales) or ()."""
+    if stream is None:
+        out = _short().append(q_new, k_new, v_new, cu_new, k_pages, v_pages,
+                              *(scales or (None, None)), page_table, seq_lens, rope_cos, rope_sin,
+                              q_weight, k_weight, eps, interleaved, page_size, q_out)
+        if out is not None:
+            return _answer(out, name)[0]
     k_st = _token_rows(k_new, "k_new")
     dev = k_new.get_device()
     total, H_kv, d = shape = k_new.shape
@@ -979,6 +1031,11 @@ def fa_decode_paged_fp8(q, k_pages, v_pages, k_scales, v_scales, page_table, seq
     torch.float8_e4m3fn with scales [P,H_kv,page_size/block] fp32, page_table
     packed [n] or a block table [B, max_pages] -> o [B,H,d] bf16; `lse` [B,H]
     fp32 is filled where it is given."""
+    if stream is None:
+        out = _short().decode(q, k_pages, v_pages, k_scales, v_scales, page_table, seq_lens,
+                              page_size, scale, o, lse)
+        if out is not None:
+            return _answer(out, "fa_decode_paged_fp8")[0]
     _check(q, "q", torch.bfloat16, 3)
     dev = q.get_device()
     B, H, d = shape = q.shape

@@ -365,3 +365,56 @@ def test_a_token_all_the_way(interleaved, table):
         assert rms <= 2.0 ** -3
         assert ((lse[b].double().view(Hk, -1) - torch.logsumexp(s, -1)).abs() <=
                 off.amax(-1) + 1e-3).all()
+
+
+def test_the_binding_s_two_ways_agree():
+    """A call on the current stream takes the binding's short way, one with the
+    stream given by hand the long one: same bits, outputs given or not."""
+    g = torch.Generator().manual_seed(3)
+    T, H, Hk, d = 70, 6, 2, 128
+    x = torch.randn((T, (H + 2 * Hk) * d), generator=g).bfloat16().cuda()
+    q, k, v = (t.view(T, -1, d) for t in x.split([H * d, Hk * d, Hk * d], 1))
+    w = torch.nn.Parameter(1 + 0.2 * torch.randn(d, generator=g).cuda())
+    here = torch.cuda.current_stream()
+    pairs = []
+
+    def both(f, *a, **kw):
+        out = [f(*a, **kw), f(*a, stream=here, **kw)]
+        _ok()
+        pairs.append([o if isinstance(o, tuple) else (o,) for o in out])
+        return out[0]
+
+    cos, sin = both(fa.fa_rope_table, 512, 64, 1e4, "linear", 2.0)
+    pos = torch.randint(0, 512, (T,), generator=g).int().cuda()
+    both(fa.fa_qk_norm_rope, q, k, w, w, cos, sin, pos, interleaved=True)
+    both(fa.fa_qk_norm_rope, q.transpose(0, 1)[None].contiguous(),
+         k.transpose(0, 1)[None].contiguous(), None, w, cos, sin)
+    both(fa.fa_qk_norm_rope, q, k, q_out=torch.empty_like(q), k_out=torch.empty_like(k))
+    both(fa.fa_qk_norm_rope_bwd, q, k, q, k, w, None, cos, sin, pos)
+    cu = torch.tensor([0, 50, 70]).int().cuda()
+    c = Cache([300, 100], H, Hk, d, 64, "packed", seed=2)
+    t = c.table.cuda()
+    for dt in (torch.bfloat16, FP8):
+        pools = []
+        for stream in (None, here):
+            kp, vp = (torch.zeros((5, Hk, PS, d), device="cuda").to(dt) for _ in range(2))
+            ks, vs = (torch.ones((5, Hk, 4), device="cuda") for _ in range(2))
+            a = (q, k, v, cu, kp, vp) + (() if dt is torch.bfloat16 else (ks, vs))
+            f = fa.fa_append_paged_rope if dt is torch.bfloat16 else fa.fa_append_paged_fp8
+            out = f(*a, t, c.seq, cos, sin, w, w, stream=stream)
+            f(None, *a[1:], t, c.seq, cos, sin, None, w, stream=stream)
+            _ok()
+            pools.append((out, kp.view(torch.uint8), vp.view(torch.uint8), ks, vs))
+        pairs.append(pools)
+    for table in (t, torch.stack([t[:2], t[2:3].expand(2)]).contiguous()):
+        both(fa.fa_decode_paged_fp8, c.q, c.kp, c.vp, c.ks, c.vs, table, c.seq)
+        both(fa.fa_decode_paged_fp8, c.q, c.kp, c.vp, c.ks, c.vs, table, c.seq, scale=0.3,
+             lse=torch.empty(c.q.shape[:2], device="cuda"), o=torch.empty_like(c.q))
+    for a, b in pairs:
+        assert len(a) == len(b)
+        for y, z in zip(a, b):
+            assert (y is None and z is None) or torch.equal(y, z)
+    for bad in (dict(eps=-1.0), dict(q_weight=w[:64])):
+        for stream in (None, here):
+            with pytest.raises((fa.FaError, ValueError)):
+                fa.fa_qk_norm_rope(q, k, rope_cos=cos, rope_sin=sin, stream=stream, **bad)
