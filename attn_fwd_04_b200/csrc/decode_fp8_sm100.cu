@@ -84,11 +84,37 @@ __device__ __forceinline__ int pages_of(int len) {
 }
 __device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
 
-// One sequence a thread: its table base, usable length and the tiles before it.
+// A sequence's table base, usable length and the tiles before it.
 struct Slice {
     int64_t base, tiles_before;
     int len;
 };
+
+// Inclusive prefix over a warp's lanes.
+__device__ __forceinline__ int64_t warp_prefix(int64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t n = __shfl_up_sync(0xffffffffu, v, o);
+        if ((threadIdx.x & 31) >= o) v += n;
+    }
+    return v;
+}
+
+// Up to 32 sequences, one a lane (every warp for itself); `total`: their tiles.
+__device__ __forceinline__ Slice scan_warp(const DecodeFp8& p, int64_t& total) {
+    const int i = threadIdx.x & 31;
+    const int len = i < p.B ? __ldg(p.lens + i) : 0;
+    Slice s;
+    s.base = p.max_pages ? static_cast<int64_t>(i) * p.max_pages
+                         : warp_prefix(pages_of(len)) - pages_of(len);
+    bool bad;
+    s.len = usable_len(p, len, s.base, bad);
+    if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
+    const int64_t upto = warp_prefix(tiles_of(s.len));
+    s.tiles_before = upto - tiles_of(s.len);
+    total = __shfl_sync(0xffffffffu, upto, 31);
+    return s;
+}
 
 struct ScanShared {
     int64_t sum[kWarps];
@@ -97,12 +123,7 @@ struct ScanShared {
 // Exclusive prefix over the block of one value a thread; `total` of the block.
 __device__ __forceinline__ int64_t block_prefix(int64_t v, ScanShared& sh, int64_t& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t n = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += n;
-    }
+    int64_t inc = warp_prefix(v);
     if (lane == 31) sh.sum[warp] = inc;
     __syncthreads();
     total = 0;
@@ -115,7 +136,8 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, ScanShared& sh, int64
     return inc - v;
 }
 
-// Sequences first .. first + kThreads - 1, with the pages and tiles before them.
+// More of them: sequences first .. first + kThreads - 1, one a thread, with the
+// pages and tiles before them.
 __device__ __forceinline__ Slice scan_chunk(const DecodeFp8& p, int first, int64_t& pages,
                                             int64_t& tiles, ScanShared& sh) {
     const int i = first + threadIdx.x;
@@ -136,16 +158,22 @@ __device__ __forceinline__ Slice scan_chunk(const DecodeFp8& p, int first, int64
     return s;
 }
 
+// a / b, by a 32-bit division where that will do (a short stream's latency).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // The stream is cut into as many ranges as there are warps, but no empty ones.
 __device__ __forceinline__ int ranges_of(const DecodeFp8& p, int64_t T) {
     return static_cast<int>(min(static_cast<int64_t>(p.ranges), T));
 }
 // Range r of `ranges` equal ones of T tiles, and the range that holds tile t.
 __device__ __forceinline__ int64_t range_start(int64_t r, int64_t T, int ranges) {
-    return r * T / ranges;
+    return quotient(r * T, ranges);
 }
 __device__ __forceinline__ int64_t range_of(int64_t t, int64_t T, int ranges) {
-    return ((t + 1) * ranges - 1) / T;
+    return quotient((t + 1) * ranges - 1, T);
 }
 
 // ---- fragments ------------------------------------------------------------------
@@ -240,7 +268,7 @@ __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
-    fa_decode_fp8_split_kernel(const DecodeFp8 p) {
+    fa_decode_fp8_split_kernel(const __grid_constant__ DecodeFp8 p) {
     constexpr int KJ = D / 64;   // 16-byte loads of a token's K for each lane
     constexpr int VW = D / 32;   // words of a token's V for each lane
     constexpr int MT = D / 16;   // 16-row tiles of O^T
@@ -251,41 +279,59 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.launch_dependents;");
 
-    int64_t pages = 0, tiles = 0;
-    Slice s = scan_chunk(p, 0, pages, tiles, scan);
-    for (int first = kThreads; first < p.B; first += kThreads)
-        scan_chunk(p, first, pages, tiles, scan);
-    const int64_t T = tiles * p.Hk;
-    if (T == 0) return;
-    const int ranges = ranges_of(p, T);
     // consecutive ranges on different CTAs, so that a few spread over the SMs
     const int wid = warp * gridDim.x + blockIdx.x;
     const int r = wid / p.groups, group = wid - r * p.groups;
-    pages = tiles = 0;
-    for (int first = 0; first < p.B; first += kThreads) {
-        if (p.B > kThreads) s = scan_chunk(p, first, pages, tiles, scan);
+    int64_t T, start;
+    int ranges;
+    Slice mine;  // the sequence in which this warp's range begins
+    Cursor c;
+    if (p.B <= 32) {
+        mine = scan_warp(p, T);
+        T *= p.Hk;
+        ranges = ranges_of(p, T);
+        if (r >= ranges) return;
+        start = range_start(r, T, ranges);
+        const bool here = start >= mine.tiles_before * p.Hk &&
+                          start < (mine.tiles_before + tiles_of(mine.len)) * p.Hk;
+        c.b = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+        mine.base = __shfl_sync(0xffffffffu, mine.base, c.b);
+        mine.tiles_before = __shfl_sync(0xffffffffu, mine.tiles_before, c.b);
+        mine.len = __shfl_sync(0xffffffffu, mine.len, c.b);
+    } else {
+        int64_t pages = 0, tiles = 0;
+        Slice s = scan_chunk(p, 0, pages, tiles, scan);
+        for (int first = kThreads; first < p.B; first += kThreads)
+            scan_chunk(p, first, pages, tiles, scan);
+        T = tiles * p.Hk;
+        if (T == 0) return;
+        ranges = ranges_of(p, T);
+        pages = tiles = 0;
+        for (int first = 0; first < p.B; first += kThreads) {
+            if (p.B > kThreads) s = scan_chunk(p, first, pages, tiles, scan);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const int64_t at =
-                range_start((w * gridDim.x + blockIdx.x) / p.groups, T, ranges);
-            if (at >= s.tiles_before * p.Hk && at < (s.tiles_before + tiles_of(s.len)) * p.Hk) {
-                found[w] = s;
-                found_b[w] = first + threadIdx.x;
+            for (int w = 0; w < kWarps; ++w) {
+                const int64_t at =
+                    range_start((w * gridDim.x + blockIdx.x) / p.groups, T, ranges);
+                if (at >= s.tiles_before * p.Hk &&
+                    at < (s.tiles_before + tiles_of(s.len)) * p.Hk) {
+                    found[w] = s;
+                    found_b[w] = first + threadIdx.x;
+                }
             }
         }
+        __syncthreads();
+        if (r >= ranges) return;
+        start = range_start(r, T, ranges);
+        mine = found[warp];
+        c.b = found_b[warp];
     }
-    __syncthreads();
-    if (r >= ranges) return;
-    const int64_t start = range_start(r, T, ranges);
     int64_t left = range_start(r + 1, T, ranges) - start;
-
-    Cursor c;
-    c.b = found_b[warp];
-    c.len = found[warp].len;
-    c.base = found[warp].base;
+    c.len = mine.len;
+    c.base = mine.base;
     c.tiles = tiles_of(c.len);
-    const int64_t in_seq = start - found[warp].tiles_before * p.Hk;
-    c.hk = static_cast<int>(in_seq / c.tiles);
+    const int64_t in_seq = start - mine.tiles_before * p.Hk;
+    c.hk = static_cast<int>(quotient(in_seq, c.tiles));
     c.tile = static_cast<int>(in_seq - static_cast<int64_t>(c.hk) * c.tiles);
     enter_head(p, c);
 
@@ -548,86 +594,121 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 
 // One (sequence, query head) a CTA: the pieces of a head that the ranges cut,
 // o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M); and what has no tokens.
+// A warp takes every fourth piece, kBatch of them in flight with their sums,
+// each warp with a running maximum of its own.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) fa_decode_fp8_merge_kernel(const DecodeFp8 p,
-                                                                            int slots) {
+__global__ void __launch_bounds__(kMergeThreads)
+    fa_decode_fp8_merge_kernel(const __grid_constant__ DecodeFp8 p, int slots) {
     static_assert(kMergeThreads == kThreads, "the scan's block");
-    constexpr int V = D / 32;
+    constexpr int V = D / 32, kBatch = 8;
     __shared__ ScanShared scan;
     __shared__ Slice mine_sh;
-    __shared__ float red[kWarps], acc_sh[kWarps][D], w_sh[kWarps];
+    __shared__ float acc_sh[kWarps][D], top_sh[kWarps], sum_sh[kWarps];
     const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t pages = 0, tiles = 0;
-    for (int first = 0; first < p.B; first += kThreads) {
-        const Slice s = scan_chunk(p, first, pages, tiles, scan);
-        if (first + static_cast<int>(threadIdx.x) == b) mine_sh = s;
+    int64_t T, before;
+    int len;
+    if (p.B <= 32) {
+        const Slice s = scan_warp(p, T);
+        before = __shfl_sync(0xffffffffu, s.tiles_before, b);
+        len = __shfl_sync(0xffffffffu, s.len, b);
+    } else {
+        int64_t pages = 0;
+        T = 0;
+        for (int first = 0; first < p.B; first += kThreads) {
+            const Slice s = scan_chunk(p, first, pages, T, scan);
+            if (first + static_cast<int>(threadIdx.x) == b) mine_sh = s;
+        }
+        __syncthreads();
+        before = mine_sh.tiles_before;
+        len = mine_sh.len;
     }
-    __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t row = static_cast<int64_t>(b) * p.H + h;
-    const int n = tiles_of(mine_sh.len);
+    const int n = tiles_of(len);
+    const int hk = h / p.G, hg = h - hk * p.G, group = hg / p.group_heads;
+    const int hh = hg - group * p.group_heads;
+    T *= p.Hk;
+    const int64_t t0 = before * p.Hk + static_cast<int64_t>(hk) * n;
+    const int ranges = ranges_of(p, T);
+    int64_t r0 = 0, r1 = 0;
+    bool from_start = true;
+    if (n > 0) {
+        r0 = range_of(t0, T, ranges);
+        r1 = range_of(t0 + n - 1, T, ranges);
+        from_start = range_start(r0, T, ranges) == t0;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n == 0) {
         if (threadIdx.x < D) p.o[row * D + threadIdx.x] = __float2bfloat16(0.f);
         if (threadIdx.x == 0 && p.lse) p.lse[row] = -INFINITY;
         return;
     }
-    const int hk = h / p.G, hg = h - hk * p.G, group = hg / p.group_heads;
-    const int hh = hg - group * p.group_heads;
-    const int64_t T = tiles * p.Hk, t0 = mine_sh.tiles_before * p.Hk + static_cast<int64_t>(hk) * n;
-    const int ranges = ranges_of(p, T);
-    const int64_t r0 = range_of(t0, T, ranges), r1 = range_of(t0 + n - 1, T, ranges);
     if (r0 == r1) return;  // the warp wrote it
     const int pieces = static_cast<int>(r1 - r0) + 1;
-    const bool from_start = range_start(r0, T, ranges) == t0;
-    auto slot = [&](int i) {
-        const int64_t w = (r0 + i) * p.groups + group;
-        return (2 * w + (i == 0 && !from_start)) * slots + hh;
-    };
-    float top = -INFINITY;
-    for (int i = threadIdx.x; i < pieces; i += kMergeThreads)
-        top = fmaxf(top, p.part_lse[slot(i)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, red[w]);
-    if (top == -INFINITY) top = 0.f;
-    float acc[V], sum = 0.f;
+    float top = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < pieces; i += kWarps) {
-        const int64_t s = slot(i);
-        const float w = ex2_approx(p.part_lse[s] - top);
-        const float* src = p.part_o + s * D + V * lane;
-        sum += w;
-        if constexpr (V == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(src);
-            acc[0] = fmaf(w, x.x, acc[0]);
-            acc[1] = fmaf(w, x.y, acc[1]);
-            acc[2] = fmaf(w, x.z, acc[2]);
-            acc[3] = fmaf(w, x.w, acc[3]);
-        } else {
-            const float2 x = *reinterpret_cast<const float2*>(src);
-            acc[0] = fmaf(w, x.x, acc[0]);
-            acc[1] = fmaf(w, x.y, acc[1]);
+    for (int i0 = warp; i0 < pieces; i0 += kWarps * kBatch) {
+        float lse[kBatch], x[kBatch][V];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int i = i0 + k * kWarps;
+            lse[k] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[k][j] = 0.f;
+            if (i >= pieces) continue;
+            const int64_t w = (r0 + i) * p.groups + group;
+            const int64_t s = (2 * w + (i == 0 && !from_start)) * slots + hh;
+            lse[k] = p.part_lse[s];
+            const float* src = p.part_o + s * D + V * lane;
+            if constexpr (V == 4) {
+                const float4 y = *reinterpret_cast<const float4*>(src);
+                x[k][0] = y.x;
+                x[k][1] = y.y;
+                x[k][2] = y.z;
+                x[k][3] = y.w;
+            } else {
+                const float2 y = *reinterpret_cast<const float2*>(src);
+                x[k][0] = y.x;
+                x[k][1] = y.y;
+            }
+        }
+        float m = top;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) m = fmaxf(m, lse[k]);
+        const float base = m == -INFINITY ? 0.f : m, keep = ex2_approx(top - base);
+        top = m;
+        sum *= keep;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] *= keep;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const float w = ex2_approx(lse[k] - base);
+            sum += w;
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = fmaf(w, x[k][j], acc[j]);
         }
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) acc_sh[warp][V * lane + j] = acc[j];
-    if (lane == 0) w_sh[warp] = sum;
+    if (lane == 0) {
+        top_sh[warp] = top;
+        sum_sh[warp] = sum;
+    }
     __syncthreads();
     if (threadIdx.x < D) {
-        float a = 0.f, l = 0.f;
+        float m = top_sh[0], a = 0.f, l = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, top_sh[w]);
+        const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            a += acc_sh[w][threadIdx.x];
-            l += w_sh[w];
+            const float f = ex2_approx(top_sh[w] - base);
+            a = fmaf(f, acc_sh[w][threadIdx.x], a);
+            l = fmaf(f, sum_sh[w], l);
         }
         p.o[row * D + threadIdx.x] = __float2bfloat16(l == 0.f ? 0.f : a / l);
-        if (threadIdx.x == 0 && p.lse) p.lse[row] = (top + log2f(l)) * 0.69314718055994531f;
+        if (threadIdx.x == 0 && p.lse) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
     }
 }
 
