@@ -29,6 +29,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 16;  // of a CTA, at most, where rows are taken one by one
 constexpr int kRows = 4;     // of a thread at a time
+constexpr int kFewRows = 1;  // the same where sequences have a few new tokens each
 constexpr int kStages = 4;   // 8-bit pages: chunks of new rows on their way, less one
 constexpr int kRing = kStages * kRows * kThreads * 16;  // bytes of shared memory
 
@@ -56,7 +57,7 @@ struct Append {
 struct Seq {
     int b, row0, n, len;
     int64_t page_base;
-    bool found, bad;
+    bool bad;
 };
 
 // Lengths may be anything up to 2^31 - 1, and so may their sums be wrong: page
@@ -96,11 +97,11 @@ __device__ __forceinline__ int page_at(const Append& p, const Seq& s, int pos) {
 
 struct Shared {
     int64_t units[kWarps], pages[kWarps];
-    int64_t page_base;
-    int b, blk;
-    // rows: of each token, its sequence, that one's page base; position and page
+    Seq seq_of_unit;
+    int blk;
+    // rows: of each token, its sequence; position and page
     int seq[kTokens];
-    int64_t base[kTokens];
+    Seq of[kTokens];
     int pos[kTokens], page[kTokens];
 };
 
@@ -138,8 +139,8 @@ __device__ __forceinline__ void place_rows(const Append& p, int first, int count
         int r0 = 0, n = 0, len = 0;
         if (i < p.B) {
             bool bad;
-            rows_of(p, i, r0, n, bad);
             len = __ldg(p.lens + i);
+            rows_of(p, i, r0, n, bad);
             if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
         }
         const int lo = max(r0, first), hi = min(r0 + n, first + count);
@@ -152,17 +153,14 @@ __device__ __forceinline__ void place_rows(const Append& p, int first, int count
             pages += total;
         }
         for (int r = lo; r < hi; ++r)
-            if (sh.seq[r - first] == i) sh.base[r - first] = base;
+            if (sh.seq[r - first] == i)
+                sh.of[r - first] = Seq{i, r0, n, len, base, seq_bad(p, n, len, base)};
     }
     __syncthreads();
     if (threadIdx.x < count && sh.seq[threadIdx.x] >= 0) {
-        Seq s{};
-        s.b = sh.seq[threadIdx.x];
-        rows_of(p, s.b, s.row0, s.n, s.bad);
-        s.len = __ldg(p.lens + s.b);
-        s.page_base = sh.base[threadIdx.x];
+        const Seq s = sh.of[threadIdx.x];
         int pos = -1, page = -1;
-        if (seq_bad(p, s.n, s.len, s.page_base)) {
+        if (s.bad) {
             record_error(p.err, FA_DEVERR_BAD_INPUT);
         } else {
             pos = s.len - s.n + (first + static_cast<int>(threadIdx.x) - s.row0);
@@ -324,14 +322,14 @@ __device__ __forceinline__ bool find_unit(const Append& p, int unit, Shared& sh,
     const int lg = p.block_log2;
     int64_t before = 0, pages = 0;  // of the sequences scanned
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (threadIdx.x == 0) sh.b = -1;
+    if (threadIdx.x == 0) sh.blk = -1;
     for (int base = 0; base < p.B; base += kThreads) {
         const int i = base + threadIdx.x;
         int c = 0, np = 0, r0 = 0, n = 0, len = 0;
-        bool bad = false;
         if (i < p.B) {
-            rows_of(p, i, r0, n, bad);
+            bool bad;
             len = __ldg(p.lens + i);
+            rows_of(p, i, r0, n, bad);
             np = pages_of(len);
             if (bad || n > len) {  // no units, but its pages count
                 record_error(p.err, FA_DEVERR_BAD_INPUT);
@@ -365,24 +363,18 @@ __device__ __forceinline__ bool find_unit(const Append& p, int unit, Shared& sh,
             all_pages += sh.pages[w];
         }
         if (unit >= before + ci - c && unit < before + ci) {
-            sh.b = i;
-            sh.blk = static_cast<int>(unit - (before + ci - c));
-            sh.page_base = pages + pi - np;
+            const int64_t first_page = pages + pi - np;
+            sh.blk = ((len - n) >> lg) + static_cast<int>(unit - (before + ci - c));
+            sh.seq_of_unit = Seq{i, r0, n, len, first_page, seq_bad(p, n, len, first_page)};
         }
         before += all_units;
         pages += all_pages;
         __syncthreads();
         if (before > unit) break;
     }
-    s = Seq{};
-    s.b = sh.b;
-    s.found = s.b >= 0;
-    if (!s.found) return false;
-    rows_of(p, s.b, s.row0, s.n, s.bad);
-    s.len = __ldg(p.lens + s.b);
-    s.page_base = sh.page_base;
-    s.bad = s.bad || seq_bad(p, s.n, s.len, s.page_base);
-    blk = ((s.len - s.n) >> lg) + sh.blk;
+    blk = sh.blk;
+    if (blk < 0) return false;
+    s = sh.seq_of_unit;
     if (s.bad && threadIdx.x == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
     return !s.bad;
 }
@@ -643,53 +635,70 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
 
 // A block where sequences have a few new tokens each, as in a decode step: each
 // slot takes one head of K or of V (pairs pair_begin .. pair_end - 1, the keys
-// first), kRows tokens at a time, and finds its scale alone; where scales grow,
+// first), kFewRows tokens at a time, and finds its scale alone; where scales grow,
 // the CTA rounds the earlier tokens of those heads together.
 template <int D, bool INTER>
-__device__ __forceinline__ void append_few(const Append& p, const Block& b, int pair_begin,
+__device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block b, int pair_begin,
                                            int pair_end) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     __shared__ float ratio[SL];  // of each slot's head; 0: nothing to round again
     const Lane<D, INTER> lane(p.t.half);
     const int my = threadIdx.x / LPR;
-    const int rows = b.last - b.first, chunks = (rows + kRows - 1) / kRows;
+    const int rows = b.last - b.first, chunks = (rows + kFewRows - 1) / kFewRows;
     const int per_page = kPage >> p.block_log2;
     Vec8 w = {};
     if (p.wk.w) w = lane.weights(p.wk);
+    // the first rows and positions, on their way while the page is looked up
+    auto rows_at = [&](int pair) {
+        return (pair < p.Hk ? p.k + b.row * p.sk + pair * D
+                            : p.v + b.row * p.sv + (pair - p.Hk) * D);
+    };
+    uint4 raw[kFewRows];
+    Rotation<D, INTER> rot[kFewRows];
+    auto fetch = [&](int pair, int c) {
+        const __nv_bfloat16* x = rows_at(pair);
+        const int64_t sx = pair < p.Hk ? p.sk : p.sv;
+#pragma unroll
+        for (int u = 0; u < kFewRows; ++u) {
+            const int r = c * kFewRows + u;
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (r < rows) {
+                raw[u] = lane.load(x + r * sx);
+                rot[u].load(p.t, b.first + r, lane);
+            }
+        }
+    };
+    fetch(min(pair_begin + my, pair_end - 1), 0);
+    const int page = page_at(p, s, b.lo);
+    if (page < 0) return;
+    b.slice0 = static_cast<int64_t>(page) * p.Hk;
     for (int base = pair_begin; base < pair_end; base += SL) {
         const bool live = base + my < pair_end;
         const int pair = live ? base + my : pair_end - 1;
         const bool is_k = pair < p.Hk;
         const int h = is_k ? pair : pair - p.Hk;
-        const int64_t sx = is_k ? p.sk : p.sv;
-        const __nv_bfloat16* x = (is_k ? p.k : p.v) + b.row * sx + h * D;
         float* scale = (is_k ? p.ks : p.vs) + (b.slice0 + h) * per_page + (b.at >> p.block_log2);
         float was = 0.f;
         if (b.first > b.lo && lane.chunk == 0) was = *scale;
         was = __shfl_sync(0xffffffffu, was, threadIdx.x & 31 & ~(LPR - 1));
-        Vec8 v[kRows];
+        Vec8 v[kFewRows];
         auto take = [&](int c) {
+            if (c > 0 || base > pair_begin) fetch(pair, c);
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int r = c * kRows + u;
-                v[u] = lane.unpack(r < rows ? lane.load(x + r * sx) : make_uint4(0, 0, 0, 0));
-            }
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
+            for (int u = 0; u < kFewRows; ++u) {
+                v[u] = lane.unpack(raw[u]);
                 if (p.wk.w) {  // a warp's slots may be of keys and of values
                     const Vec8 n = norm_row<D>(v[u], w, p.eps);
                     if (is_k) v[u] = n;
                 }
-                Rotation<D, INTER> rot;
-                rot.load(p.t, min(b.first + c * kRows + u, b.last - 1), lane);
-                if (is_k) rot.apply(v[u]);
+                if (is_k && c * kFewRows + u < rows) rot[u].apply(v[u]);
             }
         };
         float amax = 0.f, odd = 0.f;
         for (int c = 0; c < chunks; ++c) {
             take(c);
             float o;
-            amax = fmaxf(amax, finite_max<D, INTER, kRows>(v, o));
+            amax = fmaxf(amax, finite_max<D, INTER, kFewRows>(v, o));
             odd = fmaxf(odd, o);
         }
 #pragma unroll
@@ -700,10 +709,13 @@ __device__ __forceinline__ void append_few(const Append& p, const Block& b, int 
                        ((b.slice0 + h) * kPage + b.at) * D;
         if (live && lane.chunk == 0) *scale = now;
         for (int c = chunks - 1; c >= 0; --c) {
-            if (c < chunks - 1) take(c);
+            if (c < chunks - 1) {
+                fetch(pair, c);
+                take(c);
+            }
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) {
-                const int r = c * kRows + u;
+            for (int u = 0; u < kFewRows; ++u) {
+                const int r = c * kFewRows + u;
                 if (live && r < rows)
                     lane.store(dst + (b.first - b.lo + r) * D, codes8<D, INTER>(v[u], now, simple_scale(now, odd)));
             }
@@ -736,9 +748,9 @@ __device__ __forceinline__ void append_few(const Append& p, const Block& b, int 
     }
 }
 
-// The block of unit `unit`; false: none, or none that can be taken.
-__device__ __forceinline__ bool find_block(const Append& p, int unit, Shared& sh, Block& b) {
-    Seq s;
+// The block of unit `unit` (without its page); false: none that can be taken.
+__device__ __forceinline__ bool find_block(const Append& p, int unit, Shared& sh, Seq& s,
+                                           Block& b) {
     int blk = 0;
     if (!find_unit(p, unit, sh, s, blk)) return false;
     const int start = s.len - s.n;
@@ -747,9 +759,7 @@ __device__ __forceinline__ bool find_block(const Append& p, int unit, Shared& sh
     b.last = min(b.lo + (1 << p.block_log2), s.len);
     b.row = s.row0 + (b.first - start);
     b.at = b.lo % kPage;
-    const int page = page_at(p, s, b.lo);
-    b.slice0 = static_cast<int64_t>(page) * p.Hk;
-    return page >= 0;
+    return true;
 }
 
 // The first CTAs take units, unit_ctas of them: for each unit as many as
@@ -768,12 +778,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int hgroups = (p.Hk + p.unit_heads - 1) / p.unit_heads;
     const int per_unit = FEW ? (2 * p.Hk + p.unit_heads - 1) / p.unit_heads : 2 * hgroups;
     const int unit = cta / per_unit, sub = cta - unit * per_unit;
+    Seq s;
     Block b;
-    if (!find_block(p, unit, sh, b)) return;
+    if (!find_block(p, unit, sh, s, b)) return;
     if constexpr (FEW) {
         const int first = sub * p.unit_heads;
-        append_few<D, INTER>(p, b, first, min(first + p.unit_heads, 2 * p.Hk));
+        append_few<D, INTER>(p, s, b, first, min(first + p.unit_heads, 2 * p.Hk));
     } else {
+        const int page = page_at(p, s, b.lo);
+        if (page < 0) return;
+        b.slice0 = static_cast<int64_t>(page) * p.Hk;
         const bool is_k = sub < hgroups;
         const int first = (is_k ? sub : sub - hgroups) * p.unit_heads;
         const int end = min(first + p.unit_heads, p.Hk);
