@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "rope_row.cuh"
@@ -475,102 +476,122 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, bool take) {
 }
 
 // The CTA's slots times kRows are CH rows: a head's CH tokens at a time (larger
-// blocks in chunks), or the block's tokens of CH / block heads at once.  A
-// thread's rows are of kRows / UH heads, UH rows each, UH = block / slots; where
-// a block has fewer tokens than there are slots (16 tokens of 64 values), the
-// first half of the CTA's warps and the second take heads of their own.
-template <int D, bool INTER, int UH>
+// blocks, MANY, in chunks), or the block's tokens of CH / block heads at once.  A
+// thread's rows are of NH = kRows / UH heads, UH rows each, UH = block / slots;
+// where a block has half as many tokens as there are slots (16 tokens of 64
+// values), PARTS = 2: the first half of the warps and the second take heads of
+// their own.  Row u is token tok + (u % UH) * slots of the chunk, of head
+// h + part + (u / UH) * PARTS.
+template <int D, bool INTER, int UH, int PARTS, bool MANY>
 __device__ __forceinline__ void append_block(const Append& p, const Block& b, bool is_k,
                                              int h_begin, int h_end, uint4* ring) {
     constexpr int LPR = D / 8, SL = kThreads / LPR, CH = SL * kRows, NH = kRows / UH;
+    constexpr int HEADS = NH * PARTS;  // at once
     __shared__ float red[2][NH][kWarps];
     const Lane<D, INTER> lane(p.t.half);
-    const int block = 1 << p.block_log2;
     const int my = threadIdx.x / LPR;
-    const int parts = UH == 1 && block < SL ? SL / block : 1;  // of the CTA, with heads of their own
-    const int part = parts > 1 ? my / block : 0, tok = parts > 1 ? my % block : my;
-    const int at_once = NH * parts;  // heads
-    const int rows = b.last - b.first, chunks = UH == kRows ? (rows + CH - 1) / CH : 1;
+    const int part = PARTS > 1 ? my / (SL / PARTS) : 0, tok = PARTS > 1 ? my % (SL / PARTS) : my;
+    const int rows = b.last - b.first, chunks = MANY ? (rows + CH - 1) / CH : 1;
     const bool norms = is_k && p.wk.w;
     Vec8 w = {};
     if (norms) w = lane.weights(p.wk);
     Rotation<D, INTER> rot[UH];
-    int turned = -1;  // the chunk that `rot` is of
+    // Where the thread's tokens of chunk c lie, and which of them there are: rows
+    // behind the last are that one again, and are not stored.
     const int64_t sx = is_k ? p.sk : p.sv;
-    const __nv_bfloat16* x0 = (is_k ? p.k : p.v) + (b.row + tok) * sx + part * D;
-    // row u of this thread: token tok + (u % UH) * SL of the chunk, head h + part
-    // + (u / UH) * parts
+    const __nv_bfloat16* x0 = (is_k ? p.k : p.v) + b.row * sx;
+    const __nv_bfloat16* src[UH];
+    uint32_t there = 0;
+    auto aim = [&](int c, int h) {
+#pragma unroll
+        for (int i = 0; i < UH; ++i)
+            src[i] = x0 + min(c * CH + i * SL + tok, rows - 1) * sx + h * D;
+    };
+    auto place = [&](int c) {
+        there = 0;
+#pragma unroll
+        for (int i = 0; i < UH; ++i) {
+            if (c * CH + i * SL + tok < rows) there |= 1u << i;
+            if (is_k)
+                rot[i].load(p.t, min(b.first + c * CH + i * SL + tok, b.last - 1), lane);
+        }
+    };
     // A ring of chunks on their way: a slot's rows are copied, and read, by its
     // own lanes, so that a warp waits for nothing but its own copies.
     int ask_h = h_begin, ask_c = 0, ask_at = 0, at = 0;
+    uint4* const mine_in_ring = ring + threadIdx.x;
     auto ask = [&]() {
         if (ask_h < h_end) {
-            const __nv_bfloat16* x = x0 + ask_c * CH * sx + ask_h * D + 8 * lane.chunk;
-            uint4* dst = ring + ask_at * (kRows * kThreads) + threadIdx.x;
+            uint4* dst = mine_in_ring + ask_at * (kRows * kThreads);
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
-                const bool take = ask_c * CH + (u % UH) * SL + tok < rows &&
-                                  ask_h + part + (u / UH) * parts < h_end;
-                copy16(dst + u * kThreads,
-                       take ? x + (u % UH) * SL * sx + (u / UH) * parts * D : p.k, take);
+                const __nv_bfloat16* x = src[u % UH] + (u / UH) * PARTS * D + 8 * lane.chunk;
+                const bool head = HEADS == 1 || ask_h + part + (u / UH) * PARTS < h_end;
+                copy16(dst + u * kThreads, head ? x : p.k, head);
             }
-            if (++ask_c == chunks) {
-                ask_c = 0;
-                ask_h += at_once;
+            if (MANY) {
+                if (++ask_c == chunks) {
+                    ask_c = 0;
+                    ask_h += HEADS;
+                }
+                aim(ask_c, ask_h + part);
+            } else {
+                ask_h += HEADS;
+#pragma unroll
+                for (int i = 0; i < UH; ++i) src[i] += HEADS * D;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         ask_at = ask_at + 1 == kStages ? 0 : ask_at + 1;
     };
     Vec8 v[kRows];
-    auto turn = [&](int c) {  // v's rows, of chunk c, normed and rotated
+    auto turn = [&]() {  // v's rows normed and rotated
         if (norms) {
 #pragma unroll
             for (int u = 0; u < kRows; ++u) v[u] = norm_row<D>(v[u], w, p.eps);
         }
-        if (!is_k) return;
-        if (turned != c) {
-            turned = c;
-#pragma unroll
-            for (int u = 0; u < UH; ++u)
-                rot[u].load(p.t, min(b.first + c * CH + u * SL + tok, b.last - 1), lane);
-        }
-        if (lane.turns) {
+        if (is_k && lane.turns) {
 #pragma unroll
             for (int u = 0; u < kRows; ++u) rot[u % UH].turn(v[u]);
         }
     };
-    auto take = [&](int c) {
+    const uint4* const slot_in_ring = ring + my * LPR;
+    auto take = [&]() {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncwarp();
-        const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(
-            ring + at * (kRows * kThreads) + my * LPR);
+        const uint4* stage = slot_in_ring + at * (kRows * kThreads);
+        const __nv_bfloat16* lo = reinterpret_cast<const __nv_bfloat16*>(stage) + lane.lo;
+        const __nv_bfloat16* hi = reinterpret_cast<const __nv_bfloat16*>(stage) + lane.hi;
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
-            const __nv_bfloat16* r = row + u * (kThreads * 8);
-            const uint2 lo = *reinterpret_cast<const uint2*>(r + lane.lo);
-            const uint2 hi = *reinterpret_cast<const uint2*>(r + lane.hi);
-            v[u] = lane.unpack(make_uint4(lo.x, lo.y, hi.x, hi.y));
+            const uint2 l = *reinterpret_cast<const uint2*>(lo + u * (kThreads * 8));
+            const uint2 h = *reinterpret_cast<const uint2*>(hi + u * (kThreads * 8));
+            v[u] = lane.unpack(make_uint4(l.x, l.y, h.x, h.y));
         }
         at = at + 1 == kStages ? 0 : at + 1;
-        turn(c);
+        turn();
         ask();  // into the stage read before this one
     };
     const int per_page = kPage >> p.block_log2;
-    float* scales = (is_k ? p.ks : p.vs) + b.slice0 * per_page + (b.at >> p.block_log2);
-    uint8_t* codes = static_cast<uint8_t*>(is_k ? p.kp : p.vp) + (b.slice0 * kPage + b.at) * D;
+    float* scale = (is_k ? p.ks : p.vs) + (b.slice0 + h_begin + part) * per_page +
+                   (b.at >> p.block_log2);
+    uint8_t* const codes = static_cast<uint8_t*>(is_k ? p.kp : p.vp);
+    uint8_t* dst = codes + ((b.slice0 + h_begin + part) * kPage + b.at + (b.first - b.lo) + tok) * D;
+    aim(0, h_begin + part);
+    place(0);
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) ask();
-    for (int h = h_begin; h < h_end; h += at_once) {
+    for (int h = h_begin; h < h_end; h += HEADS) {
         float was[NH], amax[NH], odd[NH];
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-            const int head = h + part + n * parts;
-            was[n] = b.first > b.lo && head < h_end ? scales[head * per_page] : 0.f;
+            const bool head = HEADS == 1 || h + part + n * PARTS < h_end;
+            was[n] = b.first > b.lo && head ? scale[n * PARTS * per_page] : 0.f;
             amax[n] = odd[n] = 0.f;
         }
         for (int c = 0; c < chunks; ++c) {
-            take(c);
+            if (MANY) place(c);
+            take();
 #pragma unroll
             for (int n = 0; n < NH; ++n) {
                 float o;
@@ -578,7 +599,7 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
                 odd[n] = fmaxf(odd[n], o);
             }
         }
-        float(&mine)[NH][kWarps] = red[(h - h_begin) / at_once & 1];  // two: one barrier will do
+        float(&mine)[NH][kWarps] = red[(h - h_begin) / HEADS & 1];  // two: one barrier will do
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
             // (bits of non-negative floats are in their order)
@@ -586,33 +607,34 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
             if ((threadIdx.x & 31) == 0) mine[n][threadIdx.x >> 5] = __uint_as_float(top);
         }
         __syncthreads();  // every thread has read the old scales
-        const int warps = kWarps / parts;
+        bool simple = true;
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-            const int head = h + part + n * parts;
+            constexpr int warps = kWarps / PARTS;
+            const bool head = HEADS == 1 || h + part + n * PARTS < h_end;
+#pragma unroll
             for (int i = 0; i < warps; ++i) amax[n] = fmaxf(amax[n], mine[n][part * warps + i]);
             const float now = fmaxf(was[n], least_scale(amax[n]));
-            if (head < h_end && tok == 0 && lane.chunk == 0) scales[head * per_page] = now;
+            if (head && tok == 0 && lane.chunk == 0) scale[n * PARTS * per_page] = now;
             amax[n] = now;  // the scale from here on
-            if (b.first > b.lo && head < h_end && now != was[n])  // now is a power of two
-                rescale_rows<D, INTER>(codes + static_cast<int64_t>(head) * (kPage * D),
-                                       b.first - b.lo, was[n] * inverse_power(now), tok,
-                                       SL / parts, lane);
+            simple = simple && simple_scale(now, odd[n]);
+            if (b.first > b.lo && head && now != was[n])  // now is a power of two
+                rescale_rows<D, INTER>(
+                    codes + ((b.slice0 + h + part + n * PARTS) * kPage + b.at) * D,
+                    b.first - b.lo, was[n] * inverse_power(now), tok, SL / PARTS, lane);
         }
         // the new tokens: the last chunk's values are still there
         for (int c = chunks - 1; c >= 0; --c) {
-            if (c < chunks - 1) {
-                const __nv_bfloat16* x = x0 + c * CH * sx + h * D;
+            if (MANY && c < chunks - 1) {
+                place(c);
+                const __nv_bfloat16* x = x0 + (c * CH + tok) * sx + h * D;
 #pragma unroll
                 for (int u = 0; u < kRows; ++u) {  // (only the last chunk has rows missing)
                     v[u] = lane.unpack(lane.load(x));
                     x += SL * sx;
                 }
-                turn(c);
+                turn();
             }
-            bool simple = true;
-#pragma unroll
-            for (int n = 0; n < NH; ++n) simple = simple && simple_scale(amax[n], odd[n]);
             uint2 out[kRows];
             if (simple) {
 #pragma unroll
@@ -623,13 +645,24 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
                     out[u] = codes8<D, INTER>(v[u], amax[u / UH],
                                               simple_scale(amax[u / UH], odd[u / UH]));
             }
-            uint8_t* dst = codes + static_cast<int64_t>(h + part) * (kPage * D) +
-                           (b.first - b.lo + c * CH + tok) * D;
+            uint8_t *lo = dst + c * CH * D + lane.lo, *hi = dst + c * CH * D + lane.hi;
 #pragma unroll
-            for (int u = 0; u < kRows; ++u)
-                if (c * CH + (u % UH) * SL + tok < rows && h + part + (u / UH) * parts < h_end)
-                    lane.store(dst + (u % UH) * SL * D + (u / UH) * parts * (kPage * D), out[u]);
+            for (int u = 0; u < kRows; ++u) {
+                constexpr int kHead = PARTS * kPage * D;
+                const int off = (u % UH) * SL * D + (u / UH) * kHead;
+                if ((there >> (u % UH) & 1) &&
+                    (HEADS == 1 || h + part + (u / UH) * PARTS < h_end)) {
+                    if (INTER) {
+                        *reinterpret_cast<uint2*>(lo + off) = out[u];
+                    } else {
+                        *reinterpret_cast<uint32_t*>(lo + off) = out[u].x;
+                        *reinterpret_cast<uint32_t*>(hi + off) = out[u].y;
+                    }
+                }
+            }
         }
+        scale += HEADS * per_page;
+        dst += HEADS * kPage * D;
     }
 }
 
@@ -793,9 +826,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int end = min(first + p.unit_heads, p.Hk);
         constexpr int SL = kThreads / (D / 8);
         const int block = 1 << p.block_log2;
-        if (block <= SL) append_block<D, INTER, 1>(p, b, is_k, first, end, ring);
-        else if (block == 2 * SL) append_block<D, INTER, 2>(p, b, is_k, first, end, ring);
-        else append_block<D, INTER, 4>(p, b, is_k, first, end, ring);
+        auto run = [&](auto uh, auto parts, auto many) {
+            append_block<D, INTER, decltype(uh)::value, decltype(parts)::value,
+                         decltype(many)::value>(p, b, is_k, first, end, ring);
+        };
+        using std::integral_constant;
+        if (D == 64 && block < SL)
+            run(integral_constant<int, 1>{}, integral_constant<int, D == 64 ? 2 : 1>{},
+                std::false_type{});
+        else if (block == SL)
+            run(integral_constant<int, 1>{}, integral_constant<int, 1>{}, std::false_type{});
+        else if (block == 2 * SL)
+            run(integral_constant<int, 2>{}, integral_constant<int, 1>{}, std::false_type{});
+        else if (block == 4 * SL)
+            run(integral_constant<int, 4>{}, integral_constant<int, 1>{}, std::false_type{});
+        else
+            run(integral_constant<int, 4>{}, integral_constant<int, 1>{}, std::true_type{});
     }
 }
 
