@@ -31,7 +31,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 16;  // of a CTA, at most, where rows are taken one by one
 constexpr int kRows = 4;     // of a thread at a time
 constexpr int kFewRows = 1;  // the same where sequences have a few new tokens each
-constexpr int kStages = 4;   // 8-bit pages: chunks of new rows on their way, less one
+constexpr int kStages = 3;   // 8-bit pages: chunks of new rows on their way, less one
 constexpr int kRing = kStages * kRows * kThreads * 16;  // bytes of shared memory
 
 struct Append {
@@ -190,13 +190,20 @@ __device__ __forceinline__ void append_rows(const Append& p, int cta, Shared& sh
     struct Where {
         int tok, kind, h0, rows;  // kind 0: query, 1: key, 2: value
     };
-    auto where = [&](int i) {
+    int tok_ = my / groups, g_ = my - tok_ * groups;
+    const int step_tok = SL / groups, step_g = SL - step_tok * groups;
+    auto next_slot = [&]() {  // this thread's next one; no rows behind the last
         Where w;
-        w.tok = i / groups;
-        const int g = i - w.tok * groups;
-        w.kind = g < gq ? 0 : g < gq + gk ? 1 : 2;
-        w.h0 = (w.kind == 0 ? g : w.kind == 1 ? g - gq : g - gq - gk) * kRows;
-        w.rows = i < slots ? min(kRows, (w.kind == 0 ? p.H : p.Hk) - w.h0) : 0;
+        w.tok = tok_;
+        w.kind = g_ < gq ? 0 : g_ < gq + gk ? 1 : 2;
+        w.h0 = (w.kind == 0 ? g_ : w.kind == 1 ? g_ - gq : g_ - gq - gk) * kRows;
+        w.rows = tok_ < count ? min(kRows, (w.kind == 0 ? p.H : p.Hk) - w.h0) : 0;
+        tok_ += step_tok;
+        g_ += step_g;
+        if (g_ >= groups) {
+            g_ -= groups;
+            ++tok_;
+        }
         return w;
     };
     uint4 next[kRows];
@@ -209,7 +216,7 @@ __device__ __forceinline__ void append_rows(const Append& p, int cta, Shared& sh
         for (int u = 0; u < kRows; ++u)
             if (u < w.rows) next[u] = lane.load(x + u * D);
     };
-    Where w = where(my);
+    Where w = next_slot();
     fetch(w);
     place_rows(p, first, count, sh);
     const bool norms = p.wq.w || p.wk.w;
@@ -218,7 +225,7 @@ __device__ __forceinline__ void append_rows(const Append& p, int cta, Shared& sh
 #pragma unroll
         for (int u = 0; u < kRows; ++u) raw[u] = next[u];
         const Where now = w;
-        w = where(i + SL);
+        w = next_slot();
         fetch(w);
         if (now.rows == 0 && !norms) continue;
         const int tok = min(now.tok, count - 1);
@@ -259,7 +266,7 @@ __device__ __forceinline__ void append_rows(const Append& p, int cta, Shared& sh
 }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) fa_append_rope_kernel(const __grid_constant__ Append p) {
+__global__ void __launch_bounds__(kThreads, 3) fa_append_rope_kernel(const __grid_constant__ Append p) {
     __shared__ Shared sh;
     append_rows<D, INTER, true>(p, blockIdx.x, sh);
 }
@@ -529,12 +536,12 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
                 const bool head = HEADS == 1 || ask_h + part + (u / UH) * PARTS < h_end;
                 copy16(dst + u * kThreads, head ? x : p.k, head);
             }
-            if (MANY) {
-                if (++ask_c == chunks) {
+            if (MANY) {  // a head's chunks up to the last one, and back to the first
+                if (++ask_c == 2 * chunks - 1) {
                     ask_c = 0;
                     ask_h += HEADS;
                 }
-                aim(ask_c, ask_h + part);
+                aim(min(ask_c, 2 * chunks - 2 - ask_c), ask_h + part);
             } else {
                 ask_h += HEADS;
 #pragma unroll
@@ -627,13 +634,7 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
         for (int c = chunks - 1; c >= 0; --c) {
             if (MANY && c < chunks - 1) {
                 place(c);
-                const __nv_bfloat16* x = x0 + (c * CH + tok) * sx + h * D;
-#pragma unroll
-                for (int u = 0; u < kRows; ++u) {  // (only the last chunk has rows missing)
-                    v[u] = lane.unpack(lane.load(x));
-                    x += SL * sx;
-                }
-                turn();
+                take();
             }
             uint2 out[kRows];
             if (simple) {
@@ -754,8 +755,9 @@ __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block 
             }
         }
         if (b.first == b.lo) continue;  // the same for the CTA
-        if (lane.chunk == 0) ratio[my] = live && now != was ? was * inverse_power(now) : 0.f;
-        __syncthreads();
+        const bool grows = live && now != was;
+        if (lane.chunk == 0) ratio[my] = grows ? was * inverse_power(now) : 0.f;
+        if (!__syncthreads_or(grows)) continue;
         // rows of all the slots' heads, kFew of them in flight for each slot
         constexpr int kFew = 8;
         const int old = b.first - b.lo, all = min(SL, pair_end - base) * old;
@@ -922,20 +924,27 @@ int launch_rope(const Append& p, cudaStream_t st) {
 
 template <int D, bool INTER>
 int launch_fp8(Append& p, int num_sms, cudaStream_t st) {
-    // Sequences with a few tokens each: a slot takes a head, and as many heads go
-    // to a CTA as make two CTAs an SM.  Else up to 16 heads of a unit one after
-    // the other, and fewer where SMs would be short of CTAs.
-    const int64_t heads = static_cast<int64_t>(p.units) * 2 * p.Hk;
+    // Sequences with a few tokens each: a slot takes a head, and a unit's heads go
+    // to as many CTAs as make two an SM, the rows' CTAs among them (a step of 64
+    // tokens 6.3 us, with one CTA too many an SM 8.1).  Else up to 16 heads of a
+    // unit one after the other, and fewer where SMs would be short of CTAs.
+    const int row_ctas = p.q ? (p.total + p.tokens - 1) / p.tokens : 0;
     const bool few = p.total <= static_cast<int64_t>(p.B) * kRows;
-    int64_t each = few ? (heads + num_sms * 2 - 1) / (num_sms * 2) : heads / (num_sms * 3);
-    // (a CTA takes 64 rows of 128 values, or 128 of 64, at once)
-    const int at_once = few ? 1 : std::max(1, kThreads * kRows * 8 / D >> p.block_log2);
-    each = std::min<int64_t>(std::max<int64_t>(each, 1), 16);
-    each = std::min<int64_t>((each + at_once - 1) / at_once * at_once, few ? 2 * p.Hk : p.Hk);
+    int64_t each;
+    if (few) {
+        const int per_unit = std::max(1, std::max(num_sms, 2 * num_sms - row_ctas) / p.units);
+        each = std::max(1, (2 * p.Hk + per_unit - 1) / per_unit);
+    } else {
+        // (a CTA takes 64 rows of 128 values, or 128 of 64, at once)
+        const int at_once = std::max(1, kThreads * kRows * 8 / D >> p.block_log2);
+        each = static_cast<int64_t>(p.units) * 2 * p.Hk / (num_sms * 3);
+        each = std::min<int64_t>(std::max<int64_t>(each, 1), 16);
+        each = std::min<int64_t>((each + at_once - 1) / at_once * at_once, p.Hk);
+    }
     p.unit_heads = static_cast<int>(each);
     p.unit_ctas = p.units * static_cast<int>(few ? (2 * p.Hk + each - 1) / each
                                                  : 2 * ((p.Hk + each - 1) / each));
-    const int ctas = p.unit_ctas + (p.q ? (p.total + p.tokens - 1) / p.tokens : 0);
+    const int ctas = p.unit_ctas + row_ctas;
     if (few) {
         fa_append_fp8_kernel<D, INTER, true><<<ctas, kThreads, 0, st>>>(p);
     } else {
