@@ -127,8 +127,9 @@ struct NormRope {
 // where tokens come first, the tokens of a group where heads do.
 struct Slot {
     int b, n, h0;
-    __device__ __forceinline__ Slot(const NormRope& p, const Side& s, uint32_t i, int U) {
-        if (p.heads_first) {
+    __device__ __forceinline__ Slot(const NormRope& p, const Side& s, uint32_t i, int U,
+                                    bool heads_first) {
+        if (heads_first) {
             const uint32_t outer = p.N.quotient(i);
             n = static_cast<int>(i - outer * p.N.d);
             b = static_cast<int>(s.groups.quotient(outer));
@@ -150,7 +151,9 @@ struct Slot {
 
 // The grid's first CTAs take the queries, the others the keys, each in equal
 // strides over its slots: a CTA's weights stay in registers.
-template <int D, bool INTER, int U>
+// (HEADS: heads first; else the heads of a token are D apart, which makes every
+// row's address a constant offset.)
+template <int D, bool INTER, bool HEADS, int U>
 __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const __grid_constant__ NormRope p) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     const Lane<D, INTER> lane(p.t.half);
@@ -165,15 +168,14 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const __grid_
          base += stride) {
         const uint32_t i = base + threadIdx.x / LPR;
         const bool live = i < s.slots;
-        const Slot at(p, s, live ? i : s.slots - 1, U);
+        const Slot at(p, s, live ? i : s.slots - 1, U, HEADS);
         const int count = s.heads - at.h0;  // of rows, U at most
         uint4 raw[U];
         const __nv_bfloat16* x = s.x + s.rx.at(at.b, at.n, at.h0);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             raw[u] = make_uint4(0, 0, 0, 0);
-            if (u < count) raw[u] = lane.load(x);
-            x += s.rx.head;
+            if (u < count) raw[u] = lane.load(x + u * (HEADS ? s.rx.head : D));
         }
         bool bad;
         const int pos = at.position(p, bad);
@@ -194,8 +196,9 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const __grid_
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (live && u < count) lane.store(y, bad ? make_uint4(0, 0, 0, 0) : lane.pack(v[u]));
-            y += s.ry.head;
+            if (live && u < count)
+                lane.store(y + u * (HEADS ? s.ry.head : D),
+                           bad ? make_uint4(0, 0, 0, 0) : lane.pack(v[u]));
         }
     }
 }
@@ -205,12 +208,13 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const __grid_
 // x is read again and normed again: cheaper than a saved statistic.  Each
 // thread sums dw over its rows in registers, the CTA over its threads in
 // shared memory, and a second kernel over the CTAs in fp64: a fixed order.
-template <int D, bool INTER, int U>
+template <int D, bool INTER, bool HEADS, int U>
 __global__ void __launch_bounds__(kThreads, kBwdCtas)
     fa_norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     __shared__ float red[SL][D];
     const Lane<D, INTER> lane(p.t.half);
+    asm volatile("griddepcontrol.launch_dependents;");
     const bool is_q = static_cast<int>(blockIdx.x) < p.q.ctas;
     const Side& s = is_q ? p.q : p.k;
     const uint32_t stride = static_cast<uint32_t>(s.ctas) * SL;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
          base += stride) {
         const uint32_t i = base + threadIdx.x / LPR;
         const bool live = i < s.slots;
-        const Slot at(p, s, live ? i : s.slots - 1, U);
+        const Slot at(p, s, live ? i : s.slots - 1, U, HEADS);
         const int count = s.heads - at.h0;
         uint4 gr[U], xr[U];
         const __nv_bfloat16* g = s.g + s.rg.at(at.b, at.n, at.h0);
@@ -230,11 +234,9 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
         for (int u = 0; u < U; ++u) {
             gr[u] = xr[u] = make_uint4(0, 0, 0, 0);
             if (u < count) {
-                gr[u] = lane.load(g);
-                if (norms) xr[u] = lane.load(x);
+                gr[u] = lane.load(g + u * (HEADS ? s.rg.head : D));
+                if (norms) xr[u] = lane.load(x + u * (HEADS ? s.rx.head : D));
             }
-            g += s.rg.head;
-            x += s.rx.head;
         }
         bool bad;
         const int pos = at.position(p, bad);
@@ -268,8 +270,9 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
                 }
                 gv = scale8(gv, r);
             }
-            if (mine) lane.store(y, bad ? make_uint4(0, 0, 0, 0) : lane.pack(gv));
-            y += s.ry.head;
+            if (mine)
+                lane.store(y + u * (HEADS ? s.ry.head : D),
+                           bad ? make_uint4(0, 0, 0, 0) : lane.pack(gv));
         }
     }
     if (!norms) return;  // the whole CTA
@@ -290,26 +293,29 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
     }
 }
 
-// dw of q (block 0) and of k (block 1): the CTAs' partial sums added in fp64.
-constexpr int kSumRows = 8;
+// dw, kSumCols values of it a block, q's first: the CTAs' partial sums added in
+// fp64.  Launched while the last CTAs of the kernel before it still run.
+constexpr int kSumCols = 32, kSumRows = 32;
 template <int D>
-__global__ void __launch_bounds__(D* kSumRows)
-    fa_norm_rope_dw_kernel(const float* __restrict__ part, int q_ctas, int ctas,
-                           float* __restrict__ dwq, float* __restrict__ dwk) {
-    __shared__ double red[kSumRows][D];
-    const int col = threadIdx.x % D, row = threadIdx.x / D;
-    float* dst = blockIdx.x == 0 ? dwq : dwk;
+__global__ void __launch_bounds__(kSumCols* kSumRows)
+    fa_norm_rope_dw_kernel(const float* part, int q_ctas, int ctas, float* __restrict__ dwq,
+                           float* __restrict__ dwk) {
+    __shared__ double red[kSumRows][kSumCols];
+    const bool is_q = blockIdx.x < D / kSumCols;
+    float* dst = is_q ? dwq : dwk;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (dst == nullptr) return;
-    const int end = blockIdx.x == 0 ? q_ctas : ctas;
+    const int col = blockIdx.x % (D / kSumCols) * kSumCols + threadIdx.x;
+    const int end = is_q ? q_ctas : ctas;
     double s = 0.0;
 #pragma unroll 8
-    for (int i = (blockIdx.x == 0 ? 0 : q_ctas) + row; i < end; i += kSumRows)
+    for (int i = (is_q ? 0 : q_ctas) + threadIdx.y; i < end; i += kSumRows)
         s += part[static_cast<int64_t>(i) * D + col];
-    red[row][col] = s;
+    red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (row == 0) {
+    if (threadIdx.y == 0) {
 #pragma unroll
-        for (int i = 1; i < kSumRows; ++i) s += red[i][col];
+        for (int i = 1; i < kSumRows; ++i) s += red[i][threadIdx.x];
         dst[col] = static_cast<float>(s);
     }
 }
@@ -403,16 +409,32 @@ int set_grid(NormRope& p, int64_t tokens, int d, int heads_per_slot, int per_sm,
 
 template <int D, bool INTER>
 int launch_norm(const NormRope& p, int ctas, cudaStream_t st) {
-    fa_norm_rope_kernel<D, INTER, kFwdHeads><<<ctas, kThreads, 0, st>>>(p);
+    if (p.heads_first) fa_norm_rope_kernel<D, INTER, true, kFwdHeads><<<ctas, kThreads, 0, st>>>(p);
+    else fa_norm_rope_kernel<D, INTER, false, kFwdHeads><<<ctas, kThreads, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D, bool INTER>
 int launch_norm_bwd(const NormRope& p, int ctas, float* dwq, float* dwk, cudaStream_t st) {
-    fa_norm_rope_bwd_kernel<D, INTER, kBwdHeads><<<ctas, kThreads, 0, st>>>(p);
-    if (p.part)
-        fa_norm_rope_dw_kernel<D><<<2, D * kSumRows, 0, st>>>(p.part, p.q.ctas, ctas, dwq, dwk);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+    if (p.heads_first)
+        fa_norm_rope_bwd_kernel<D, INTER, true, kBwdHeads><<<ctas, kThreads, 0, st>>>(p);
+    else
+        fa_norm_rope_bwd_kernel<D, INTER, false, kBwdHeads><<<ctas, kThreads, 0, st>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (!p.part) return FA_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * D / kSumCols);
+    cfg.blockDim = dim3(kSumCols, kSumRows);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fa_norm_rope_dw_kernel<D>, static_cast<const float*>(p.part),
+                              p.q.ctas, ctas, dwq, dwk) == cudaSuccess
+               ? FA_OK
+               : FA_ERR_CUDA;
 }
 
 }  // namespace
