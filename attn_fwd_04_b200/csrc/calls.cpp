@@ -208,19 +208,15 @@ PyObject* tuple_of(std::initializer_list<Tensor> ts) {
     return out;
 }
 
-// Runs `f`; an exception of any kind becomes a Python error or None, and what is
-// not the ordinary case None.
+// Runs `f`; what is not the ordinary case, and an exception (no memory, no GPU: all
+// before the launch), becomes None, and the long way meets it again.
 template <class F>
 PyObject* call(Py_ssize_t n, Py_ssize_t want, F f) {
     if (n != want || !g_bound) Py_RETURN_NONE;
     try {
         return f();
-    } catch (const Other&) {
-        Py_RETURN_NONE;
-    } catch (const std::exception& e) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
     } catch (...) {
+        if (PyErr_Occurred()) return nullptr;
         Py_RETURN_NONE;
     }
 }

@@ -192,6 +192,94 @@ def test_append_fp8(table, interleaved, new, ctx, H, Hk, d, R, weights, block):
     _check_fp8(c, before, interleaved)
 
 
+@pytest.mark.parametrize("H,Hk,d,R,weights,block", [
+    (5, 5, 128, 128, "fp32", 16), (3, 3, 128, 64, "none", 32), (20, 20, 128, 16, "bf16", 64),
+    (9, 9, 64, 64, "fp32", 16), (5, 5, 64, 16, "none", 64), (3, 3, 64, 48, "bf16", 128),
+    (2, 2, 64, 64, "fp32", 256), (1, 1, 128, 128, "fp32", 256)])
+@pytest.mark.parametrize("new,ctx", [([300, 0, 70, 5], [40, 9, 250, 0]), ([900], [13]),
+                                     ([4, 2, 3], [62, 255, 14])], ids=range(3))
+def test_append_fp8_shapes(new, ctx, H, Hk, d, R, weights, block):
+    """Every way in which a CTA's rows are divided among a block's tokens and
+    heads, heads that are left over, and sequences with a few tokens."""
+    c = Case(new, ctx, H, Hk, d, R, weights, "packed", block, seed=Hk + block)
+    before = [t.clone() for t in (c.kp, c.vp, c.ks, c.vs)]
+    q = c.call()
+    _ok()
+    _within(q, c.turned(c.q, c.qw, False))
+    _check_fp8(c, before, False)
+
+
+def test_fp8_special_values_on_the_way_of_prompts_and_of_steps():
+    """Infinities, NaN, zeros and values beyond the format's reach, with every
+    block width: the same codes as the definition's."""
+    for block in (16, 32, 64, 128, 256):
+        for new, ctx in (([150, 300], [3, 0]), ([1] * 6, [0, 20, 70, 255, 256, 300])):
+            c = Case(new, ctx, 1, 3, 128, 0, "none", "rows", block, seed=block)
+            g = torch.Generator().manual_seed(block)
+            x = c.v.float().cpu()
+            pick = torch.rand(x.shape, generator=g)
+            x[pick < 0.002] = float("inf")
+            x[(pick > 0.002) & (pick < 0.004)] = float("-inf")
+            x[(pick > 0.004) & (pick < 0.006)] = float("nan")
+            x[(pick > 0.006) & (pick < 0.2)] = 0.0
+            c.v = x.bfloat16().cuda()
+            old = c.vs.clone()
+            c.call(with_q=False)
+            _ok()
+            page, slot = c.places()
+            at = 0
+            for b, (n, cx) in enumerate(zip(new, ctx)):
+                for lo in range(cx // block * block, cx + n, block):
+                    first, last = max(lo, cx), min(lo + block, cx + n)
+                    r = slice(at + first - cx, at + last - cx)
+                    pg, blk = page[at + first - cx].item(), lo % PS // block
+                    for h in range(3):
+                        rows = c.v[r, h].double()
+                        fin = rows[rows.isfinite()]
+                        s = ref.least_scale(fin.abs().max().item() if len(fin) else 0.0)
+                        if first > lo:
+                            s = max(s, old[pg, h, blk].item())
+                        assert c.vs[pg, h, blk].item() == s
+                        got = c.vp.view(torch.uint8)[pg, h, first % PS:(last - 1) % PS + 1]
+                        want = ref.e4m3(rows / s).view(torch.uint8)
+                        nan = (want & 127) == 127
+                        assert torch.equal((got & 127) == 127, nan)
+                        assert torch.equal(got[~nan], want[~nan])
+                at += n
+
+
+def test_offsets_past_32_bits():
+    """A pool whose last pages lie more than 2^32 bytes (8-bit pages: codes) from
+    its start."""
+    for block in (0, 64):
+        c = Case([40, 1], [30, 700], 2, 4, 128, 64, "fp32", "packed", block, seed=1)
+        want = c.call()
+        small = c.kp.clone(), c.vp.clone()
+        d = Case([40, 1], [30, 700], 2, 4, 128, 64, "fp32", "packed", block, seed=1)
+        size = 1 if block else 2
+        P = (1 << 32) // (4 * PS * 128 * size) + c.P
+        far = P - c.P
+        for name in ("kp", "vp") + (("ks", "vs") if block else ()):
+            t = getattr(d, name)
+            big = torch.empty((P,) + t.shape[1:], dtype=t.dtype, device="cuda")
+            big[far:].copy_(t) if t.dtype != FP8 else \
+                big[far:].view(torch.uint8).copy_(t.view(torch.uint8))
+            setattr(d, name, big)
+        d.table = d.table + far
+        got = d.call()
+        _ok()
+        assert torch.equal(got, want)
+        for a, b in zip((d.kp, d.vp), small):
+            assert torch.equal(a[far:].view(torch.uint8), b.view(torch.uint8))
+        if block:
+            assert torch.equal(d.ks[far:], c.ks) and torch.equal(d.vs[far:], c.vs)
+            q = want[[39, 40]].repeat(1, 2, 1)
+            o = [fa.fa_decode_paged_fp8(q, x.kp, x.vp, x.ks, x.vs, x.table.cuda(), x.seq)
+                 for x in (c, d)]
+            _ok()
+            assert torch.equal(o[0], o[1])
+
+
 def test_fp8_many_sequences():
     c = Case([1] * 300, [i % 70 for i in range(300)], 2, 1, 64, 16, "none", "rows", 16, seed=9)
     before = [t.clone() for t in (c.kp, c.vp, c.ks, c.vs)]
