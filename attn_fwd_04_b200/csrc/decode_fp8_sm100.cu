@@ -15,8 +15,8 @@
 // GPU takes an equal, contiguous piece of it, whatever the lengths.  A warp
 // that holds all of a sequence's head writes the output; pieces of one that is
 // cut are written as normalised partial outputs with their log-sum-exp, which
-// the second launch joins.  There is no plan kernel: each CTA sums the lengths
-// itself while it starts.
+// the second launch joins.  There is no plan kernel: each warp (each CTA, where
+// there are many sequences) sums the lengths itself while it starts.
 //
 // Within a warp nothing goes through shared memory but the query.  The matrix
 // instruction's first operand is the cache: S^T[tokens, heads] = K Q^T and
@@ -37,6 +37,7 @@
 // rounded to fp16 (11 bits), scaled by a power of two that follows the largest
 // value scale so far, so that block scales may differ by 2^28 before small
 // ones lose bits.
+#include <algorithm>
 #include <cmath>
 
 #include "fa_internal.h"
@@ -49,7 +50,7 @@ constexpr int kPage = 256;
 constexpr int kTile = 32;  // tokens a step of a warp
 constexpr int kWarps = 4;  // a CTA
 constexpr int kThreads = kWarps * 32;
-constexpr int kMergeThreads = 128;
+constexpr int kWarpSeqs = 128;  // sequences that a warp looks through by itself, at most
 
 struct DecodeFp8 {
     const __nv_bfloat16* q;
@@ -59,6 +60,8 @@ struct DecodeFp8 {
     __nv_bfloat16* o;
     float* lse;
     float *part_o, *part_lse;  // [2 * warps, 8 * NT (, D)] pieces
+    int64_t* seqs;             // [1 + B, 2]: the stream's tiles; for each sequence the
+                               // tiles before it and its length (B > kWarpSeqs)
     int B, H, Hk, G, num_pages, table_len, max_pages, block_log2;
     int groups, group_heads;  // groups of query heads of one K/V head
     int ranges;               // warps of each group: the stream's ranges, at most
@@ -100,20 +103,34 @@ __device__ __forceinline__ int64_t warp_prefix(int64_t v) {
     return v;
 }
 
-// Up to 32 sequences, one a lane (every warp for itself); `total`: their tiles.
-__device__ __forceinline__ Slice scan_warp(const DecodeFp8& p, int64_t& total) {
-    const int i = threadIdx.x & 31;
+// Sequences first .. first + 31, one a lane, with the pages and tiles before them:
+// up to kWarpSeqs are looked at by every warp for itself, without a barrier
+// between a short batch's lengths and its first loads.
+__device__ __forceinline__ Slice scan_lanes(const DecodeFp8& p, int first, int64_t& pages,
+                                            int64_t& tiles) {
+    const int i = first + (threadIdx.x & 31);
     const int len = i < p.B ? __ldg(p.lens + i) : 0;
     Slice s;
-    s.base = p.max_pages ? static_cast<int64_t>(i) * p.max_pages
-                         : warp_prefix(pages_of(len)) - pages_of(len);
+    s.base = static_cast<int64_t>(i) * p.max_pages;
+    if (p.max_pages == 0) {
+        const int64_t upto = pages + warp_prefix(pages_of(len));
+        s.base = upto - pages_of(len);
+        pages = __shfl_sync(0xffffffffu, upto, 31);
+    }
     bool bad;
     s.len = usable_len(p, len, s.base, bad);
     if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
-    const int64_t upto = warp_prefix(tiles_of(s.len));
+    const int64_t upto = tiles + warp_prefix(tiles_of(s.len));
     s.tiles_before = upto - tiles_of(s.len);
-    total = __shfl_sync(0xffffffffu, upto, 31);
+    tiles = __shfl_sync(0xffffffffu, upto, 31);
     return s;
+}
+
+// Lane `from`'s, in every lane.
+__device__ __forceinline__ Slice of_lane(const Slice& s, int from) {
+    return Slice{__shfl_sync(0xffffffffu, s.base, from),
+                 __shfl_sync(0xffffffffu, s.tiles_before, from),
+                 __shfl_sync(0xffffffffu, s.len, from)};
 }
 
 struct ScanShared {
@@ -286,29 +303,42 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     int ranges;
     Slice mine;  // the sequence in which this warp's range begins
     Cursor c;
-    if (p.B <= 32) {
-        mine = scan_warp(p, T);
-        T *= p.Hk;
+    if (p.B <= kWarpSeqs) {
+        int64_t pages = 0, tiles = 0;
+        mine = scan_lanes(p, 0, pages, tiles);
+        for (int first = 32; first < p.B; first += 32) scan_lanes(p, first, pages, tiles);
+        T = tiles * p.Hk;
         ranges = ranges_of(p, T);
         if (r >= ranges) return;
         start = range_start(r, T, ranges);
-        const bool here = start >= mine.tiles_before * p.Hk &&
-                          start < (mine.tiles_before + tiles_of(mine.len)) * p.Hk;
-        c.b = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-        mine.base = __shfl_sync(0xffffffffu, mine.base, c.b);
-        mine.tiles_before = __shfl_sync(0xffffffffu, mine.tiles_before, c.b);
-        mine.len = __shfl_sync(0xffffffffu, mine.len, c.b);
+        pages = tiles = 0;
+        for (int first = 0;; first += 32) {  // some sequence holds tile `start`
+            if (p.B > 32) mine = scan_lanes(p, first, pages, tiles);
+            const uint32_t here = __ballot_sync(
+                0xffffffffu, start >= mine.tiles_before * p.Hk &&
+                                 start < (mine.tiles_before + tiles_of(mine.len)) * p.Hk);
+            if (here == 0 && first + 32 < p.B) continue;
+            c.b = first + __ffs(here) - 1;
+            mine = of_lane(mine, c.b - first);
+            break;
+        }
     } else {
         int64_t pages = 0, tiles = 0;
         Slice s = scan_chunk(p, 0, pages, tiles, scan);
         for (int first = kThreads; first < p.B; first += kThreads)
             scan_chunk(p, first, pages, tiles, scan);
         T = tiles * p.Hk;
-        if (T == 0) return;
         ranges = ranges_of(p, T);
+        if (blockIdx.x == 0 && threadIdx.x == 0) p.seqs[0] = tiles;
         pages = tiles = 0;
         for (int first = 0; first < p.B; first += kThreads) {
-            if (p.B > kThreads) s = scan_chunk(p, first, pages, tiles, scan);
+            s = scan_chunk(p, first, pages, tiles, scan);
+            const int i = first + threadIdx.x;
+            if (blockIdx.x == 0 && i < p.B) {  // for the merge
+                p.seqs[2 + 2 * static_cast<int64_t>(i)] = s.tiles_before;
+                p.seqs[3 + 2 * static_cast<int64_t>(i)] = s.len;
+            }
+            if (T == 0) continue;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const int64_t at =
@@ -592,38 +622,44 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
     }
 }
 
-// One (sequence, query head) a CTA: the pieces of a head that the ranges cut,
+// The pieces of a (sequence, query head) that the ranges cut,
 // o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M); and what has no tokens.
-// A warp takes every fourth piece, kBatch of them in flight with their sums,
-// each warp with a running maximum of its own.
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads)
+// ROW warps take a row's pieces in turn, kBatch of them in flight with their
+// sums, each warp with a running maximum of its own; the CTA's other warps take
+// other rows.
+constexpr int merge_warps(int row) { return row > 4 ? row : 4; }
+template <int D, int ROW>
+__global__ void __launch_bounds__(merge_warps(ROW) * 32)
     fa_decode_fp8_merge_kernel(const __grid_constant__ DecodeFp8 p, int slots) {
-    static_assert(kMergeThreads == kThreads, "the scan's block");
-    constexpr int V = D / 32, kBatch = 8;
-    __shared__ ScanShared scan;
-    __shared__ Slice mine_sh;
-    __shared__ float acc_sh[kWarps][D], top_sh[kWarps], sum_sh[kWarps];
-    const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int V = D / 32, kBatch = 8, kMergeWarps = merge_warps(ROW);
+    static_assert(kMergeWarps == ROW || ROW == 1, "a row's warps are the CTA's, or one");
+    __shared__ float acc_sh[ROW][D], top_sh[ROW], sum_sh[ROW];
+    const int lane = threadIdx.x & 31;
+    // (B * H is below 2^26)
+    const uint32_t at = (blockIdx.x * kMergeWarps + (threadIdx.x >> 5)) / ROW;
+    const int part = (threadIdx.x >> 5) % ROW;
+    if (at >= static_cast<uint32_t>(p.B) * p.H) return;  // a whole row's warps
+    const int b = static_cast<int>(at / static_cast<uint32_t>(p.H));
+    const int h = static_cast<int>(at - static_cast<uint32_t>(b) * p.H);
+    const int64_t row = at;
     int64_t T, before;
     int len;
-    if (p.B <= 32) {
-        const Slice s = scan_warp(p, T);
-        before = __shfl_sync(0xffffffffu, s.tiles_before, b);
-        len = __shfl_sync(0xffffffffu, s.len, b);
-    } else {
+    if (p.B <= kWarpSeqs) {
         int64_t pages = 0;
         T = 0;
-        for (int first = 0; first < p.B; first += kThreads) {
-            const Slice s = scan_chunk(p, first, pages, T, scan);
-            if (first + static_cast<int>(threadIdx.x) == b) mine_sh = s;
+        Slice mine{};
+        for (int first = 0; first < p.B; first += 32) {
+            const Slice s = of_lane(scan_lanes(p, first, pages, T), b % 32);
+            if (first == b / 32 * 32) mine = s;
         }
-        __syncthreads();
-        before = mine_sh.tiles_before;
-        len = mine_sh.len;
+        before = mine.tiles_before;
+        len = mine.len;
+    } else {
+        asm volatile("griddepcontrol.wait;" ::: "memory");  // the split kernel's
+        T = p.seqs[0];
+        before = p.seqs[2 + 2 * static_cast<int64_t>(b)];
+        len = static_cast<int>(p.seqs[3 + 2 * static_cast<int64_t>(b)]);
     }
-    const int64_t row = static_cast<int64_t>(b) * p.H + h;
     const int n = tiles_of(len);
     const int hk = h / p.G, hg = h - hk * p.G, group = hg / p.group_heads;
     const int hh = hg - group * p.group_heads;
@@ -637,10 +673,13 @@ __global__ void __launch_bounds__(kMergeThreads)
         r1 = range_of(t0 + n - 1, T, ranges);
         from_start = range_start(r0, T, ranges) == t0;
     }
+    // (what is above is of this call's inputs alone; nothing is written before this)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (n == 0) {
-        if (threadIdx.x < D) p.o[row * D + threadIdx.x] = __float2bfloat16(0.f);
-        if (threadIdx.x == 0 && p.lse) p.lse[row] = -INFINITY;
+        if (part == 0) {
+            for (int i = lane; i < D; i += 32) p.o[row * D + i] = __float2bfloat16(0.f);
+            if (lane == 0 && p.lse) p.lse[row] = -INFINITY;
+        }
         return;
     }
     if (r0 == r1) return;  // the warp wrote it
@@ -648,11 +687,11 @@ __global__ void __launch_bounds__(kMergeThreads)
     float top = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    for (int i0 = warp; i0 < pieces; i0 += kWarps * kBatch) {
+    for (int i0 = part; i0 < pieces; i0 += ROW * kBatch) {
         float lse[kBatch], x[kBatch][V];
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int i = i0 + k * kWarps;
+            const int i = i0 + k * ROW;
             lse[k] = -INFINITY;
 #pragma unroll
             for (int j = 0; j < V; ++j) x[k][j] = 0.f;
@@ -689,27 +728,35 @@ __global__ void __launch_bounds__(kMergeThreads)
             for (int j = 0; j < V; ++j) acc[j] = fmaf(w, x[k][j], acc[j]);
         }
     }
+    if constexpr (ROW > 1) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc_sh[warp][V * lane + j] = acc[j];
-    if (lane == 0) {
-        top_sh[warp] = top;
-        sum_sh[warp] = sum;
-    }
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float m = top_sh[0], a = 0.f, l = 0.f;
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, top_sh[w]);
-        const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2_approx(top_sh[w] - base);
-            a = fmaf(f, acc_sh[w][threadIdx.x], a);
-            l = fmaf(f, sum_sh[w], l);
+        for (int j = 0; j < V; ++j) acc_sh[part][V * lane + j] = acc[j];
+        if (lane == 0) {
+            top_sh[part] = top;
+            sum_sh[part] = sum;
         }
-        p.o[row * D + threadIdx.x] = __float2bfloat16(l == 0.f ? 0.f : a / l);
-        if (threadIdx.x == 0 && p.lse) p.lse[row] = (m + log2f(l)) * 0.69314718055994531f;
+        __syncthreads();
+        if (part > 0) return;
+        top = top_sh[0];
+#pragma unroll
+        for (int w = 1; w < ROW; ++w) top = fmaxf(top, top_sh[w]);
+        const float base = top == -INFINITY ? 0.f : top;
+        sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = 0.f;
+#pragma unroll
+        for (int w = 0; w < ROW; ++w) {
+            const float f = ex2_approx(top_sh[w] - base);
+            sum = fmaf(f, sum_sh[w], sum);
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = fmaf(f, acc_sh[w][V * lane + j], acc[j]);
+        }
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D) + lane * (V / 2);
+#pragma unroll
+    for (int j = 0; j < V; j += 2) dst[j / 2] = pack_bf16x2(acc[j] * inv, acc[j + 1] * inv);
+    if (lane == 0 && p.lse) p.lse[row] = (top + log2f(sum)) * 0.69314718055994531f;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -717,10 +764,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // How the query heads of a K/V head and the warps are cut.
 struct Shape {
     int groups, group_heads, nt, ctas, ranges;
-    size_t lse_bytes, bytes;
+    size_t seqs_bytes, lse_bytes, bytes;  // of the workspace: sequences, sums, pieces
 };
 
-Shape shape_of(int H, int H_kv, int d, int num_sms) {
+Shape shape_of(int B, int H, int H_kv, int d, int num_sms) {
     Shape s;
     const int G = H / H_kv;
     s.groups = (G + 15) / 16;
@@ -732,7 +779,8 @@ Shape shape_of(int H, int H_kv, int d, int num_sms) {
     s.ranges = s.ctas * kWarps / s.groups;
     const size_t rows = static_cast<size_t>(s.ctas) * kWarps * 2 * 8 * s.nt;
     s.lse_bytes = (rows * sizeof(float) + 255) & ~size_t{255};
-    s.bytes = s.lse_bytes + rows * d * sizeof(float);
+    s.seqs_bytes = B > kWarpSeqs ? ((2 + 2 * static_cast<size_t>(B)) * 8 + 255) & ~size_t{255} : 0;
+    s.bytes = s.seqs_bytes + s.lse_bytes + rows * d * sizeof(float);
     return s;
 }
 
@@ -741,18 +789,30 @@ int launch(const DecodeFp8& p, const Shape& s, cudaStream_t st) {
     if (s.nt == 1) fa_decode_fp8_split_kernel<D, 1><<<s.ctas, kThreads, 0, st>>>(p);
     else fa_decode_fp8_split_kernel<D, 2><<<s.ctas, kThreads, 0, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    // Pieces of a head, at most on average: the ranges, or the tiles that the table
+    // has room for.  Rows of a few pieces take a warp each (2048 rows of 4: 18.4 us
+    // in all, with 4 warps a row 22.3), others 4 (1024 rows of 19: 22.2, with one
+    // 26.0) or 16.
+    const int64_t heads = static_cast<int64_t>(p.B) * p.Hk;
+    const int64_t entries = p.max_pages ? static_cast<int64_t>(p.B) * p.max_pages : p.table_len;
+    const int64_t pieces =
+        std::min<int64_t>(p.ranges, entries * (kPage / kTile) * p.Hk) / heads + 1;
+    const int each = pieces <= 8 ? 1 : pieces <= 48 ? 4 : 16;  // warps of a row
+    const int64_t warps = static_cast<int64_t>(p.B) * p.H * each;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.H);
-    cfg.blockDim = dim3(kMergeThreads);
+    cfg.gridDim =
+        dim3(static_cast<unsigned>((warps + merge_warps(each) - 1) / merge_warps(each)));
+    cfg.blockDim = dim3(merge_warps(each) * 32);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_decode_fp8_merge_kernel<D>, p, 8 * s.nt) == cudaSuccess
-               ? FA_OK
-               : FA_ERR_CUDA;
+    auto merge = each == 1   ? fa_decode_fp8_merge_kernel<D, 1>
+                 : each == 4 ? fa_decode_fp8_merge_kernel<D, 4>
+                             : fa_decode_fp8_merge_kernel<D, 16>;
+    return cudaLaunchKernelEx(&cfg, merge, p, 8 * s.nt) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -767,7 +827,7 @@ int fa_decode_paged_fp8_workspace(int B, int H, int H_kv, int d, int* bytes) {
     unsigned int* err = nullptr;
     int num_sms = 0, rc;
     if ((rc = fa::device_error_word(&err, &num_sms)) != FA_OK) return rc;
-    const fa::Shape s = fa::shape_of(H, H_kv, d, num_sms);
+    const fa::Shape s = fa::shape_of(B, H, H_kv, d, num_sms);
     if (s.bytes > 0x7fffffff) return FA_ERR_SHAPE;
     *bytes = static_cast<int>(s.bytes);
     return FA_OK;
@@ -802,12 +862,13 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     fa::DecodeFp8 p{};
     int num_sms = 0, rc;
     if ((rc = fa::device_error_word(&p.err, &num_sms)) != FA_OK) return rc;
-    const fa::Shape s = fa::shape_of(H, H_kv, d, num_sms);
+    const fa::Shape s = fa::shape_of(B, H, H_kv, d, num_sms);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* ws = nullptr;
     if ((rc = fa::call_workspace(workspace, workspace_bytes, s.bytes, st, &ws)) != FA_OK) return rc;
-    p.part_lse = static_cast<float*>(ws);
-    p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + s.lse_bytes);
+    p.seqs = static_cast<int64_t*>(ws);
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + s.seqs_bytes);
+    p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + s.seqs_bytes + s.lse_bytes);
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.kp = static_cast<const uint8_t*>(k_pages);
     p.vp = static_cast<const uint8_t*>(v_pages);
