@@ -934,7 +934,8 @@ template <int D>
 int launch_solo(DecodeFp8& p, const Shape& s, int num_sms, cudaStream_t st) {
     const int heads = p.B * p.Hk * p.groups;
     const bool wide = s.nt == 1 && heads <= num_sms;
-    p.cluster = 8;
+    // (clusters of 8 would not all find room at once: 16 of them took 12 us and not 9)
+    p.cluster = 4;
     while (p.cluster > 1 && heads * p.cluster > num_sms) p.cluster /= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(heads) * p.cluster);
