@@ -187,6 +187,19 @@ struct Rows {
     }
 };
 
+// A call with the library's workspace of its stream; where that is refused, as it
+// is while the stream is captured, once more with scratch of the graph's own.
+template <class Run, class Bytes>
+int with_scratch(const Tensor& like, Run run, Bytes bytes_of) {
+    int rc = run(nullptr, 0);
+    if (rc != FA_ERR_UNSUPPORTED) return rc;
+    int bytes = 0;
+    rc = bytes_of(&bytes);
+    if (rc != FA_OK) return rc;
+    const Tensor ws = at::empty({bytes}, like.options().dtype(ScalarType::Byte));
+    return run(ws.data_ptr(), bytes);
+}
+
 PyObject* tuple_of(std::initializer_list<Tensor> ts) {
     PyObject* out = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
     if (!out) return nullptr;
@@ -261,19 +274,18 @@ PyObject* norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
             return g;
         };
         const Tensor dqw = grad(a[13], t.qw), dkw = grad(a[14], t.kw);
-        int bytes = 0, rc;
-        Tensor ws;
-        if (t.qw || t.kw) {
-            rc = g_fa.norm_bwd_bytes(r.B, r.N, r.H, r.Hk, r.d, &bytes);
-            if (rc != FA_OK) return PyLong_FromLong(rc);
-            ws = at::empty({bytes}, r.q.options().dtype(ScalarType::Byte));
-        }
-        rc = g_fa.norm_bwd(
-            r.q.const_data_ptr(), r.k.const_data_ptr(), gq.const_data_ptr(), gk.const_data_ptr(),
-            dq.data_ptr(), dk.data_ptr(), dqw.defined() ? dqw.data_ptr<float>() : nullptr,
-            dkw.defined() ? dkw.data_ptr<float>() : nullptr, t.qw, t.kw, t.type, t.cos, t.sin,
-            t.max_pos, t.rot, inter, r.positions, r.layout, r.B, r.N, r.H, r.Hk, r.d, r.sq, r.sk,
-            sgq, sgk, sdq, sdk, eps, ws.defined() ? ws.data_ptr() : nullptr, bytes, stream());
+        const auto run = [&](void* ws, int bytes) {
+            return g_fa.norm_bwd(
+                r.q.const_data_ptr(), r.k.const_data_ptr(), gq.const_data_ptr(),
+                gk.const_data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                dqw.defined() ? dqw.data_ptr<float>() : nullptr,
+                dkw.defined() ? dkw.data_ptr<float>() : nullptr, t.qw, t.kw, t.type, t.cos, t.sin,
+                t.max_pos, t.rot, inter, r.positions, r.layout, r.B, r.N, r.H, r.Hk, r.d, r.sq,
+                r.sk, sgq, sgk, sdq, sdk, eps, ws, bytes, stream());
+        };
+        const int rc = with_scratch(r.q, run, [&](int* bytes) {
+            return g_fa.norm_bwd_bytes(r.B, r.N, r.H, r.Hk, r.d, bytes);
+        });
         return rc != FA_OK ? PyLong_FromLong(rc) : tuple_of({dq, dk, dqw, dkw});
     });
 }
@@ -410,14 +422,15 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         float* lse =
             const_cast<float*>(static_cast<const float*>(optional(a[10], ScalarType::Float, {B, H})));
-        int bytes = 0;
-        int rc = g_fa.decode_bytes(B, H, pool.Hk, d, &bytes);
-        if (rc != FA_OK) return PyLong_FromLong(rc);
-        const Tensor ws = at::empty({bytes}, q.options().dtype(ScalarType::Byte));
-        rc = g_fa.decode(q.const_data_ptr(), pool.k.const_data_ptr(), pool.v.const_data_ptr(),
-                         s.k.const_data_ptr<float>(), s.v.const_data_ptr<float>(), s.block,
-                         table.at, table.len, table.max_pages, len_p, o.data_ptr(), lse, B, H,
-                         pool.Hk, pool.P, d, page_size, scale, ws.data_ptr(), bytes, stream());
+        const auto run = [&](void* ws, int bytes) {
+            return g_fa.decode(q.const_data_ptr(), pool.k.const_data_ptr(),
+                               pool.v.const_data_ptr(), s.k.const_data_ptr<float>(),
+                               s.v.const_data_ptr<float>(), s.block, table.at, table.len,
+                               table.max_pages, len_p, o.data_ptr(), lse, B, H, pool.Hk, pool.P, d,
+                               page_size, scale, ws, bytes, stream());
+        };
+        const int rc = with_scratch(
+            q, run, [&](int* bytes) { return g_fa.decode_bytes(B, H, pool.Hk, d, bytes); });
         return rc != FA_OK ? PyLong_FromLong(rc) : tuple_of({o});
     });
 }

@@ -470,8 +470,9 @@ int fa_rope_table(float* rope_cos, float* rope_sin, int max_pos, int rotary_dim,
         last = std::fmin(std::ceil(pair_of(low)), R - 1.0);
     }
     fa::Turns t;
+    const double log2_step = -2.0 * std::log2(base) / R;
     for (int i = 0; i < half; ++i) {
-        double w = std::pow(base, -2.0 * i / R);
+        double w = std::exp2(log2_step * i);
         double slow = 0.0;  // the share of the stretched frequency
         if (scaling == FA_ROPE_LINEAR) slow = 1.0;
         if (scaling == FA_ROPE_TURNS) {
