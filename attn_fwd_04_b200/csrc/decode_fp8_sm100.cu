@@ -32,6 +32,14 @@
 // (With the heads in the 16 rows instead, 8 heads would leave half of every
 // instruction and half of the accumulators empty.)
 //
+// 64 sequences of 1K to 32K tokens, 8 K/V heads and 32 query heads: 341 us, 6.6
+// TB/s, 1.02 of a copy, every byte read once; with 32 K/V heads and up to 16K tokens
+// 689 us, 6.7 TB/s.  Run on end for seconds the board's 1000 W bound it instead: 383
+// and 775 us at 1.6 GHz, hardly less with the products left out (384) or the
+// conversions (387).  The scheduler is 40 % busy, the tensor pipe 20 %.  A stream of
+// few tiles is bound by latency: 12 us for 8 x 2048 tokens, of which a copy would
+// take 4.
+//
 // Rounding: each query row is scaled by a power of two into fp16, which holds
 // its 8 bits exactly; scores, maxima and sums are fp32; weights p * vscale are
 // rounded to fp16 (11 bits), scaled by a power of two that follows the largest
