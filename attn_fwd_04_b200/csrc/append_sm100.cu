@@ -30,7 +30,6 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTokens = 16;  // of a CTA, at most, where rows are taken one by one
 constexpr int kRows = 4;     // of a thread at a time
-constexpr int kFewRows = 1;  // the same where sequences have a few new tokens each
 constexpr int kStages = 3;   // 8-bit pages: chunks of new rows on their way, less one
 constexpr int kRing = kStages * kRows * kThreads * 16;  // bytes of shared memory
 
@@ -84,13 +83,14 @@ __device__ __forceinline__ bool seq_bad(const Append& p, int n, int len,
     return p.max_pages ? np > p.max_pages : page_base + np > p.table_len;
 }
 
-// The page of position pos, or -1 (reported) where its index is outside the pool.
-__device__ __forceinline__ int page_at(const Append& p, const Seq& s, int pos) {
+// The page of position pos, or -1 where its index is outside the pool (reported
+// by threads that `tell`).
+__device__ __forceinline__ int page_at(const Append& p, const Seq& s, int pos, bool tell) {
     const int64_t at = p.max_pages ? static_cast<int64_t>(s.b) * p.max_pages + pos / kPage
                                    : s.page_base + pos / kPage;
     const int page = __ldg(p.table + at);
     if (page < 0 || page >= p.num_pages) {
-        if (threadIdx.x == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
+        if (tell) record_error(p.err, FA_DEVERR_BAD_INPUT);
         return -1;
     }
     return page;
@@ -165,7 +165,7 @@ __device__ __forceinline__ void place_rows(const Append& p, int first, int count
             record_error(p.err, FA_DEVERR_BAD_INPUT);
         } else {
             pos = s.len - s.n + (first + static_cast<int>(threadIdx.x) - s.row0);
-            page = page_at(p, s, pos);
+            page = page_at(p, s, pos, true);
         }
         sh.pos[threadIdx.x] = pos;
         sh.page[threadIdx.x] = page;
@@ -680,17 +680,17 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
 
 // A block where sequences have a few new tokens each, as in a decode step: each
 // slot takes one head of K or of V (pairs pair_begin .. pair_end - 1, the keys
-// first), kFewRows tokens at a time, and finds its scale alone; where scales grow,
+// first), R tokens at a time, and finds its scale alone; where scales grow,
 // the CTA rounds the earlier tokens of those heads together.  A step of 64 tokens
 // with 32 + 2 * 8 heads takes 4.9 us, as into bf16 pages.
-template <int D, bool INTER>
+template <int D, bool INTER, int R>
 __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block b, int pair_begin,
                                            int pair_end) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     __shared__ float ratio[SL];  // of each slot's head; 0: nothing to round again
     const Lane<D, INTER> lane(p.t.half);
     const int my = threadIdx.x / LPR;
-    const int rows = b.last - b.first, chunks = (rows + kFewRows - 1) / kFewRows;
+    const int rows = b.last - b.first, chunks = (rows + R - 1) / R;
     const int per_page = kPage >> p.block_log2;
     Vec8 w = {};
     if (p.wk.w) w = lane.weights(p.wk);
@@ -699,14 +699,14 @@ __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block 
         return (pair < p.Hk ? p.k + b.row * p.sk + pair * D
                             : p.v + b.row * p.sv + (pair - p.Hk) * D);
     };
-    uint4 raw[kFewRows];
-    Rotation<D, INTER> rot[kFewRows];
+    uint4 raw[R];
+    Rotation<D, INTER> rot[R];
     auto fetch = [&](int pair, int c) {
         const __nv_bfloat16* x = rows_at(pair);
         const int64_t sx = pair < p.Hk ? p.sk : p.sv;
 #pragma unroll
-        for (int u = 0; u < kFewRows; ++u) {
-            const int r = c * kFewRows + u;
+        for (int u = 0; u < R; ++u) {
+            const int r = c * R + u;
             raw[u] = make_uint4(0, 0, 0, 0);
             if (r < rows) {
                 raw[u] = lane.load(x + r * sx);
@@ -715,7 +715,7 @@ __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block 
         }
     };
     fetch(min(pair_begin + my, pair_end - 1), 0);
-    const int page = page_at(p, s, b.lo);
+    const int page = page_at(p, s, b.lo, threadIdx.x == 0);
     if (page < 0) return;
     b.slice0 = static_cast<int64_t>(page) * p.Hk;
     for (int base = pair_begin; base < pair_end; base += SL) {
@@ -727,24 +727,24 @@ __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block 
         float was = 0.f;
         if (b.first > b.lo && lane.chunk == 0) was = *scale;
         was = __shfl_sync(0xffffffffu, was, threadIdx.x & 31 & ~(LPR - 1));
-        Vec8 v[kFewRows];
+        Vec8 v[R];
         auto take = [&](int c) {
             if (c > 0 || base > pair_begin) fetch(pair, c);
 #pragma unroll
-            for (int u = 0; u < kFewRows; ++u) {
+            for (int u = 0; u < R; ++u) {
                 v[u] = lane.unpack(raw[u]);
                 if (p.wk.w) {  // a warp's slots may be of keys and of values
                     const Vec8 n = norm_row<D>(v[u], w, p.eps);
                     if (is_k) v[u] = n;
                 }
-                if (is_k && c * kFewRows + u < rows) rot[u].apply(v[u]);
+                if (is_k && c * R + u < rows) rot[u].apply(v[u]);
             }
         };
         float amax = 0.f, odd = 0.f;
         for (int c = 0; c < chunks; ++c) {
             take(c);
             float o;
-            amax = fmaxf(amax, finite_max<D, INTER, kFewRows>(v, o));
+            amax = fmaxf(amax, finite_max<D, INTER, R>(v, o));
             odd = fmaxf(odd, o);
         }
 #pragma unroll
@@ -760,10 +760,11 @@ __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block 
                 take(c);
             }
 #pragma unroll
-            for (int u = 0; u < kFewRows; ++u) {
-                const int r = c * kFewRows + u;
+            for (int u = 0; u < R; ++u) {
+                const int r = c * R + u;
                 if (live && r < rows)
-                    lane.store(dst + (b.first - b.lo + r) * D, codes8<D, INTER>(v[u], now, simple_scale(now, odd)));
+                    lane.store(dst + (b.first - b.lo + r) * D,
+                               codes8<D, INTER>(v[u], now, simple_scale(now, odd)));
             }
         }
         if (b.first == b.lo) continue;  // the same for the CTA
@@ -830,9 +831,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (!find_block(p, unit, sh, s, b)) return;
     if constexpr (FEW) {
         const int first = sub * p.unit_heads;
-        append_few<D, INTER>(p, s, b, first, min(first + p.unit_heads, 2 * p.Hk));
+        const int end = min(first + p.unit_heads, 2 * p.Hk);
+        if (b.last - b.first == 1) append_few<D, INTER, 1>(p, s, b, first, end);
+        else append_few<D, INTER, kRows>(p, s, b, first, end);
     } else {
-        const int page = page_at(p, s, b.lo);
+        const int page = page_at(p, s, b.lo, threadIdx.x == 0);
         if (page < 0) return;
         b.slice0 = static_cast<int64_t>(page) * p.Hk;
         const bool is_k = sub < hgroups;

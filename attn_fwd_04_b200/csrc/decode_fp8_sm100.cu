@@ -746,6 +746,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32, SOLO == 8 ? 1 : N
             }
         }
         if (ctas > 1) {
+            __syncwarp();
             cluster_sync_all();
             for (int at = rank * SOLO * 32 + threadIdx.x; at < heads * (D / 4);
                  at += ctas * SOLO * 32) {
@@ -760,6 +761,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32, SOLO == 8 ? 1 : N
                               return ld_cluster4(mapa_rank(smem_u32(&acc_sh[0][hh][d]), w));
                           }));
             }
+            __syncwarp();
             cluster_sync_all();  // the others may still read this CTA's
         }
     }

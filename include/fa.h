@@ -582,7 +582,7 @@ FA_API int fa_append_paged_rope(const void* q_new, const void* k_new, const void
  * sequence takes the larger of that and its present scale, and its codes are
  * rounded again when the scale grows (exact for power-of-two scales, but for
  * codes that fall below 2^-6).  Infinities, NaN and magnitudes beyond
- * 448 * 2^64 are stored as NaN.  Present scales must be positive and finite.
+ * 448 * 2^64 are stored as NaN.  Present scales must be within [2^-64, 2^64].
  * Everything else as fa_append_paged_rope; a block whose page index is out of
  * range is skipped.  block outside the list: FA_ERR_UNSUPPORTED.
  */

@@ -197,7 +197,8 @@ def test_append_fp8(table, interleaved, new, ctx, H, Hk, d, R, weights, block):
     (9, 9, 64, 64, "fp32", 16), (5, 5, 64, 16, "none", 64), (3, 3, 64, 48, "bf16", 128),
     (2, 2, 64, 64, "fp32", 256), (1, 1, 128, 128, "fp32", 256)])
 @pytest.mark.parametrize("new,ctx", [([300, 0, 70, 5], [40, 9, 250, 0]), ([900], [13]),
-                                     ([4, 2, 3], [62, 255, 14])], ids=range(3))
+                                     ([4, 2, 3], [62, 255, 14]),
+                                     ([0, 170] + [0] * 60, [3, 40] + [9] * 60)], ids=range(4))
 def test_append_fp8_shapes(new, ctx, H, Hk, d, R, weights, block):
     """Every way in which a CTA's rows are divided among a block's tokens and
     heads, heads that are left over, and sequences with a few tokens."""
@@ -435,6 +436,26 @@ def test_bad_lengths_offsets_and_pages_are_reported(block, table):
 
     c, out, before = run(offsets)
     assert torch.equal(out[:9], want[:9]) and (out[9:] == 7).all()
+
+
+@pytest.mark.parametrize("block", [0, 64])
+def test_a_bad_page_among_many_rows_is_reported(block):
+    """Prompts long enough for several tokens a CTA: the page of a single token in
+    the middle of one."""
+    new, ctx = [2000, 253, 1500], [0, 4, 100]
+    good = Case(new, ctx, 2, 1, 64, 32, "none", "packed", block, seed=3)
+    want = good.call()
+    _ok()
+    c = Case(new, ctx, 2, 1, 64, 32, "none", "packed", block, seed=3)
+    before = c.kp.clone()
+    at = ref.pages_of(good.lens)[0] + 1  # the second sequence's second page: position 256
+    page = int(c.table[at])
+    c.table[at] = -1
+    out = c.call()
+    assert fa.fa_get_device_error() == fa.FA_ERR_DEVICE_BAD_INPUT
+    assert torch.equal(out, want)
+    good.kp[page] = before[page]
+    assert torch.equal(c.kp.view(torch.uint8), good.kp.view(torch.uint8))
 
 
 def test_no_new_rows():
