@@ -214,9 +214,9 @@ __global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const __grid_
 // x is read again and normed again: cheaper than a saved statistic.  Each
 // thread sums dw over its rows in registers, the CTA over its threads in
 // shared memory, and a second kernel over the CTAs in fp64: a fixed order.
-// 36800 packed tokens of 32 + 8 heads: 208 us with the second kernel, 5.45 TB/s,
-// 0.84 of a copy; memory latency leads the stalls (3.5 of 8 cycles an instruction)
-// with the scheduler 59 % busy.
+// 36800 packed tokens of 32 + 8 heads: 196 us with the second kernel, 5.8 TB/s,
+// 0.90 of a copy; memory latency leads the stalls, with the scheduler over half
+// busy (3 heads a slot 208 us, 2 heads and 4 CTAs an SM 210, 6 and 2 242).
 template <int D, bool INTER, bool HEADS, int U>
 __global__ void __launch_bounds__(kThreads, kBwdCtas)
     fa_norm_rope_bwd_kernel(const __grid_constant__ NormRope p) {
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
         const uint32_t i = base + threadIdx.x / LPR;
         const bool live = i < s.slots;
         const Slot at(p, s, live ? i : s.slots - 1, U, HEADS);
-        const int count = s.heads - at.h0;
+        const int count = live ? s.heads - at.h0 : 0;  // rows that are not there: zeros
         uint4 gr[U], xr[U];
         const __nv_bfloat16* g = s.g + s.rg.at(at.b, at.n, at.h0);
         const __nv_bfloat16* x = s.x + s.rx.at(at.b, at.n, at.h0);
@@ -250,6 +250,10 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
         bool bad;
         const int pos = at.position(p, bad);
         if (bad && live && lane.chunk == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
+        if (bad) {  // zero gradients of the row, nothing to the weights'
+#pragma unroll
+            for (int u = 0; u < U; ++u) gr[u] = xr[u] = make_uint4(0, 0, 0, 0);
+        }
         Rotation<D, INTER> rot;
         rot.template load<true>(p.t, pos, lane);
         __nv_bfloat16* y = s.y + s.ry.at(at.b, at.n, at.h0);
@@ -257,31 +261,26 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
         for (int u = 0; u < U; ++u) {
             Vec8 gv = lane.unpack(gr[u]);
             rot.apply(gv);
-            const bool mine = live && u < count;
             if (norms) {
-                Vec8 hat = lane.unpack(xr[u]);
-                const float r = row_rstd<D>(hat, p.eps);
-                hat = scale8(hat, r);
-                if (mine && !bad) {
+                // with g' = g r:  dw += g' x,  dx = g' w - x r^2 mean(g' w x)
+                const Vec8 xv = lane.unpack(xr[u]);
+                const float r = row_rstd<D>(xv, p.eps);
+                gv = scale8(gv, r);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        acc.a[j] = f2_fma(gv.a[j], hat.a[j], acc.a[j]);
-                        acc.b[j] = f2_fma(gv.b[j], hat.b[j], acc.b[j]);
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    acc.a[j] = f2_fma(gv.a[j], xv.a[j], acc.a[j]);
+                    acc.b[j] = f2_fma(gv.b[j], xv.b[j], acc.b[j]);
                 }
                 gv = mul8(gv, w);
-                const float m = -row_sum<D>(dot8(gv, hat)) * (1.f / D);
+                const float m = row_sum<D>(dot8(gv, xv)) * (-1.f / D) * (r * r);
                 const uint64_t mm = f2_pack(m, m);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    gv.a[j] = f2_fma(hat.a[j], mm, gv.a[j]);
-                    gv.b[j] = f2_fma(hat.b[j], mm, gv.b[j]);
+                    gv.a[j] = f2_fma(xv.a[j], mm, gv.a[j]);
+                    gv.b[j] = f2_fma(xv.b[j], mm, gv.b[j]);
                 }
-                gv = scale8(gv, r);
             }
-            if (mine)
-                lane.store(y + u * (HEADS ? s.ry.head : D),
-                           bad ? make_uint4(0, 0, 0, 0) : lane.pack(gv));
+            if (u < count) lane.store(y + u * (HEADS ? s.ry.head : D), lane.pack(gv));
         }
     }
     if (!norms) return;  // the whole CTA
