@@ -306,13 +306,17 @@ __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
     enter_head(p, c);
 }
 
+// CTAs of four warps an SM, by their registers.
+constexpr int resident_ctas(int d, int nt) { return nt == 1 ? (d == 64 ? 4 : 3) : (d == 64 ? 3 : 2); }
+
 // SOLO > 0: short sequences, whose table rows hold a few pages.  A CTA of SOLO
 // warps, or a cluster of such CTAs, takes all of a sequence's head, an equal part
 // of its tiles a warp, joins the warps' results in shared memory and writes the
 // output: one launch, and no length but its own sequence's (and those before it,
 // in a packed table).
 template <int D, int NT, int SOLO>
-__global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32, SOLO == 8 ? 1 : NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
+                                  SOLO == 8 ? 1 : resident_ctas(D, NT))
     fa_decode_fp8_split_kernel(const __grid_constant__ DecodeFp8 p) {
     constexpr int KJ = D / 64;   // 16-byte loads of a token's K for each lane
     constexpr int VW = D / 32;   // words of a token's V for each lane
@@ -918,7 +922,7 @@ Shape shape_of(int B, int H, int H_kv, int d, int num_sms) {
     s.groups = (G + 15) / 16;
     s.group_heads = (G + s.groups - 1) / s.groups;
     s.nt = s.group_heads > 8 ? 2 : 1;
-    s.ctas = num_sms * (s.nt == 1 ? 3 : 2);
+    s.ctas = num_sms * resident_ctas(d, s.nt);
     const int min_ctas = (s.groups + kWarps - 1) / kWarps;
     if (s.ctas < min_ctas) s.ctas = min_ctas;  // a warp for each group
     s.ranges = s.ctas * kWarps / s.groups;
