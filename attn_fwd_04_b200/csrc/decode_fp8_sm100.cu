@@ -11,7 +11,7 @@
 // 关键术语解析, item 4.
 //
 // Two launches: split and merge.  The tokens of all sequences and K/V heads
-// form one stream of 32-token tiles, and each warp of a grid that fills the
+// form one stream of 32-token tiles (64 at d = 64), and each warp of a grid that fills the
 // GPU takes an equal, contiguous piece of it, whatever the lengths.  A warp
 // that holds all of a sequence's head writes the output; pieces of one that is
 // cut are written as normalised partial outputs with their log-sum-exp, which
@@ -55,7 +55,8 @@ namespace fa {
 namespace {
 
 constexpr int kPage = 256;
-constexpr int kTile = 32;  // tokens a step of a warp
+// Tokens a step of a warp: 8 KB of keys and values.
+constexpr int tile_tokens(int d) { return d == 64 ? 64 : 32; }
 constexpr int kWarps = 4;  // a CTA
 constexpr int kThreads = kWarps * 32;
 constexpr int kWarpSeqs = 128;  // sequences that a warp looks through by itself, at most
@@ -94,7 +95,10 @@ __device__ __forceinline__ int usable_len(const DecodeFp8& p, int len, int64_t b
 __device__ __forceinline__ int pages_of(int len) {
     return len <= 0 ? 0 : len / kPage + (len % kPage != 0);
 }
-__device__ __forceinline__ int tiles_of(int len) { return len / kTile + (len % kTile != 0); }
+template <int TILE>
+__device__ __forceinline__ int tiles_of(int len) {
+    return len / TILE + (len % TILE != 0);
+}
 
 // A sequence's table base, usable length and the tiles before it.
 struct Slice {
@@ -115,6 +119,7 @@ __device__ __forceinline__ int64_t warp_prefix(int64_t v) {
 // Sequences first .. first + 31, one a lane, with the pages and tiles before them:
 // up to kWarpSeqs are looked at by every warp for itself, without a barrier
 // between a short batch's lengths and its first loads.
+template <int TILE>
 __device__ __forceinline__ Slice scan_lanes(const DecodeFp8& p, int first, int64_t& pages,
                                             int64_t& tiles) {
     const int i = first + (threadIdx.x & 31);
@@ -129,8 +134,8 @@ __device__ __forceinline__ Slice scan_lanes(const DecodeFp8& p, int first, int64
     bool bad;
     s.len = usable_len(p, len, s.base, bad);
     if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
-    const int64_t upto = tiles + warp_prefix(tiles_of(s.len));
-    s.tiles_before = upto - tiles_of(s.len);
+    const int64_t upto = tiles + warp_prefix(tiles_of<TILE>(s.len));
+    s.tiles_before = upto - tiles_of<TILE>(s.len);
     tiles = __shfl_sync(0xffffffffu, upto, 31);
     return s;
 }
@@ -164,6 +169,7 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, ScanShared& sh, int64
 
 // More of them: sequences first .. first + kThreads - 1, one a thread, with the
 // pages and tiles before them.
+template <int TILE>
 __device__ __forceinline__ Slice scan_chunk(const DecodeFp8& p, int first, int64_t& pages,
                                             int64_t& tiles, ScanShared& sh) {
     const int i = first + threadIdx.x;
@@ -179,7 +185,7 @@ __device__ __forceinline__ Slice scan_chunk(const DecodeFp8& p, int first, int64
     bool bad;
     s.len = usable_len(p, len, s.base, bad);
     if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
-    s.tiles_before = tiles + block_prefix(tiles_of(s.len), sh, total);
+    s.tiles_before = tiles + block_prefix(tiles_of<TILE>(s.len), sh, total);
     tiles += total;
     return s;
 }
@@ -277,17 +283,19 @@ __device__ __forceinline__ int page_index(const DecodeFp8& p, const Cursor& c, i
 }
 
 // The cursor's page, and the one after it (of the same sequence) on its way.
+template <int TILE>
 __device__ __forceinline__ void enter_head(const DecodeFp8& p, Cursor& c) {
-    const int k = c.tile / (kPage / kTile);
+    const int k = c.tile / (kPage / TILE);
     c.slice = static_cast<int64_t>(page_index(p, c, k)) * p.Hk + c.hk;
     c.ahead = k < (c.len - 1) / kPage ? page_index(p, c, k + 1) : 0;
 }
 
+template <int TILE>
 __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
     if (++c.tile < c.tiles) {
-        if (c.tile % (kPage / kTile) == 0) {
+        if (c.tile % (kPage / TILE) == 0) {
             c.slice = static_cast<int64_t>(c.ahead) * p.Hk + c.hk;
-            const int k = c.tile / (kPage / kTile);
+            const int k = c.tile / (kPage / TILE);
             c.ahead = k < (c.len - 1) / kPage ? page_index(p, c, k + 1) : 0;
         }
         return;
@@ -301,13 +309,13 @@ __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
             bool bad;
             c.len = usable_len(p, __ldg(p.lens + c.b), c.base, bad);
         } while (c.len == 0 && c.b + 1 < p.B);
-        c.tiles = tiles_of(c.len);
+        c.tiles = tiles_of<TILE>(c.len);
     }
-    enter_head(p, c);
+    enter_head<TILE>(p, c);
 }
 
 // CTAs of four warps an SM, by their registers.
-constexpr int resident_ctas(int d, int nt) { return nt == 1 ? (d == 64 ? 4 : 3) : (d == 64 ? 3 : 2); }
+constexpr int resident_ctas(int nt) { return nt == 1 ? 3 : 2; }
 
 // SOLO > 0: short sequences, whose table rows hold a few pages.  A CTA of SOLO
 // warps, or a cluster of such CTAs, takes all of a sequence's head, an equal part
@@ -316,11 +324,12 @@ constexpr int resident_ctas(int d, int nt) { return nt == 1 ? (d == 64 ? 4 : 3) 
 // in a packed table).
 template <int D, int NT, int SOLO>
 __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
-                                  SOLO == 8 ? 1 : resident_ctas(D, NT))
+                                  SOLO == 8 ? 1 : resident_ctas(NT))
     fa_decode_fp8_split_kernel(const __grid_constant__ DecodeFp8 p) {
     constexpr int KJ = D / 64;   // 16-byte loads of a token's K for each lane
     constexpr int VW = D / 32;   // words of a token's V for each lane
     constexpr int MT = D / 16;   // 16-row tiles of O^T
+    constexpr int TILE = tile_tokens(D), M = TILE / 16;
     __shared__ ScanShared scan;
     __shared__ Slice found[kWarps];
     __shared__ int found_b[kWarps];
@@ -346,11 +355,11 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         bool bad;
         c.len = usable_len(p, __ldg(p.lens + c.b), c.base, bad);
         if (bad && threadIdx.x == 0) record_error(p.err, FA_DEVERR_BAD_INPUT);
-        c.tiles = tiles_of(c.len);
+        c.tiles = tiles_of<TILE>(c.len);
         const int w = rank * SOLO + warp;
         c.tile = w * c.tiles / (SOLO * ctas);
         left = (w + 1) * c.tiles / (SOLO * ctas) - c.tile;
-        if (left > 0) enter_head(p, c);
+        if (left > 0) enter_head<TILE>(p, c);
     } else {
     asm volatile("griddepcontrol.launch_dependents;");
     // consecutive ranges on different CTAs, so that a few spread over the SMs
@@ -362,18 +371,18 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
     Slice mine;  // the sequence in which this warp's range begins
     if (p.B <= kWarpSeqs) {
         int64_t pages = 0, tiles = 0;
-        mine = scan_lanes(p, 0, pages, tiles);
-        for (int first = 32; first < p.B; first += 32) scan_lanes(p, first, pages, tiles);
+        mine = scan_lanes<TILE>(p, 0, pages, tiles);
+        for (int first = 32; first < p.B; first += 32) scan_lanes<TILE>(p, first, pages, tiles);
         T = tiles * p.Hk;
         ranges = ranges_of(p, T);
         if (r >= ranges) return;
         start = range_start(r, T, ranges);
         pages = tiles = 0;
         for (int first = 0;; first += 32) {  // some sequence holds tile `start`
-            if (p.B > 32) mine = scan_lanes(p, first, pages, tiles);
+            if (p.B > 32) mine = scan_lanes<TILE>(p, first, pages, tiles);
             const uint32_t here = __ballot_sync(
                 0xffffffffu, start >= mine.tiles_before * p.Hk &&
-                                 start < (mine.tiles_before + tiles_of(mine.len)) * p.Hk);
+                                 start < (mine.tiles_before + tiles_of<TILE>(mine.len)) * p.Hk);
             if (here == 0 && first + 32 < p.B) continue;
             c.b = first + __ffs(here) - 1;
             mine = of_lane(mine, c.b - first);
@@ -381,15 +390,15 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         }
     } else {
         int64_t pages = 0, tiles = 0;
-        Slice s = scan_chunk(p, 0, pages, tiles, scan);
+        Slice s = scan_chunk<TILE>(p, 0, pages, tiles, scan);
         for (int first = kThreads; first < p.B; first += kThreads)
-            scan_chunk(p, first, pages, tiles, scan);
+            scan_chunk<TILE>(p, first, pages, tiles, scan);
         T = tiles * p.Hk;
         ranges = ranges_of(p, T);
         if (blockIdx.x == 0 && threadIdx.x == 0) p.seqs[0] = tiles;
         pages = tiles = 0;
         for (int first = 0; first < p.B; first += kThreads) {
-            s = scan_chunk(p, first, pages, tiles, scan);
+            s = scan_chunk<TILE>(p, first, pages, tiles, scan);
             const int i = first + threadIdx.x;
             if (blockIdx.x == 0 && i < p.B) {  // for the merge
                 p.seqs[2 + 2 * static_cast<int64_t>(i)] = s.tiles_before;
@@ -401,7 +410,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 const int64_t at =
                     range_start((w * gridDim.x + blockIdx.x) / p.groups, T, ranges);
                 if (at >= s.tiles_before * p.Hk &&
-                    at < (s.tiles_before + tiles_of(s.len)) * p.Hk) {
+                    at < (s.tiles_before + tiles_of<TILE>(s.len)) * p.Hk) {
                     found[w] = s;
                     found_b[w] = first + threadIdx.x;
                 }
@@ -416,22 +425,22 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
     left = range_start(r + 1, T, ranges) - start;
     c.len = mine.len;
     c.base = mine.base;
-    c.tiles = tiles_of(c.len);
+    c.tiles = tiles_of<TILE>(c.len);
     const int64_t in_seq = start - mine.tiles_before * p.Hk;
     c.hk = static_cast<int>(quotient(in_seq, c.tiles));
     c.tile = static_cast<int>(in_seq - static_cast<int64_t>(c.hk) * c.tiles);
-    enter_head(p, c);
+    enter_head<TILE>(p, c);
     }
 
     const int heads = min(p.group_heads, p.G - group * p.group_heads);  // of this group
     const int nb_log2 = 8 - p.block_log2;  // blocks of a page
-    uint32_t kr[2][2][KJ][4], vr[2][4][VW];
-    float ks[2], vs[2];
+    uint32_t kr[M][2][KJ][4], vr[M][4][VW];
+    float ks[M], vs[M];
     auto load_k = [&](const Cursor& x) {
-        const int slot0 = (x.tile * kTile) % kPage, last = slot0 + x.len - 1 - x.tile * kTile;
+        const int slot0 = (x.tile * TILE) % kPage, last = slot0 + x.len - 1 - x.tile * TILE;
         const uint8_t* base = p.kp + x.slice * (kPage * D) + 16 * t;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < M; ++m) {
             ks[m] = __ldg(p.ks + (x.slice << nb_log2) + (min(slot0 + 16 * m, last) >> p.block_log2));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -443,10 +452,10 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         }
     };
     auto load_v = [&](const Cursor& x) {
-        const int slot0 = (x.tile * kTile) % kPage, last = slot0 + x.len - 1 - x.tile * kTile;
+        const int slot0 = (x.tile * TILE) % kPage, last = slot0 + x.len - 1 - x.tile * TILE;
         const uint8_t* base = p.vp + x.slice * (kPage * D) + D / 8 * g;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < M; ++m) {
             vs[m] = __ldg(p.vs + (x.slice << nb_log2) + (min(slot0 + 16 * m, last) >> p.block_log2));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -519,16 +528,16 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
     if (SOLO > 0) __syncthreads();
     bool whole = c.tile == 0, first_piece = true;
     while (SOLO == 0 || left > 0) {
-        const int b = c.b, hk = c.hk, tok0 = c.tile * kTile, len = c.len;
+        const int b = c.b, hk = c.hk, tok0 = c.tile * TILE, len = c.len;
         const bool seg_end = c.tile + 1 == c.tiles, more = left > 1;
         --left;
-        if (more) advance(p, c);
+        if (more) advance<TILE>(p, c);
         // ---- S^T = K Q^T -------------------------------------------------------
-        float sc[NT][2][4];
+        float sc[NT][M][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[nt][m][i] = 0.f;
 #pragma unroll
@@ -541,7 +550,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
 #pragma unroll
                 for (int s2 = 0; s2 < 2; ++s2) {
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
+                    for (int m = 0; m < M; ++m) {
                         uint32_t a0, a1, a2, a3;
                         cvt4(kr[m][0][j][2 * h + s2], a0, a2);
                         cvt4(kr[m][1][j][2 * h + s2], a1, a3);
@@ -553,31 +562,39 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 }
             }
         }
-        const float k0 = ks[0], k1 = ks[1], v0 = vs[0], v1 = vs[1];
+        float k_scale[M], v_weight[M];
+        uint32_t v_most = 0;
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            k_scale[m] = ks[m];
+            v_weight[m] = vs[m];
+            v_most = max(v_most, __float_as_uint(vs[m]));
+        }
         if (more) load_k(c);
         // ---- softmax over the tile's tokens ---------------------------------------
         const float v_new = fmaxf(
-            v_top, __uint_as_float((max(__float_as_uint(v0), __float_as_uint(v1)) + 0x7fffffu) &
-                                   0x7f800000u));
+            v_top, __uint_as_float((v_most + 0x7fffffu) & 0x7f800000u));
         // 2^15 / v_new
         const float up = __uint_as_float((269u << 23) - __float_as_uint(v_new));
-        const float w0 = v0 * up, w1 = v1 * up;
+#pragma unroll
+        for (int m = 0; m < M; ++m) v_weight[m] *= up;
         bool moved = v_new != v_top;
         float keep[NT][2];
-        uint32_t pf[NT][2][2];
+        uint32_t pf[NT][M][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    sc[nt][m][i] = sc[nt][m][i] * fac[nt][i & 1] * (m ? k1 : k0);
+                    sc[nt][m][i] = sc[nt][m][i] * fac[nt][i & 1] * k_scale[m];
                     if (tok0 + 16 * m + 8 * (i >> 1) + g >= len) sc[nt][m][i] = -INFINITY;
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float top = fmaxf(fmaxf(sc[nt][0][i], sc[nt][0][i + 2]),
-                                  fmaxf(sc[nt][1][i], sc[nt][1][i + 2]));
+                float top = fmaxf(sc[nt][0][i], sc[nt][0][i + 2]);
+#pragma unroll
+                for (int m = 1; m < M; ++m) top = max3f(top, sc[nt][m][i], sc[nt][m][i + 2]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 m_run[nt][i] = m_new;
                 float sum = 0.f;
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int m = 0; m < M; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float& x = sc[nt][m][i + 2 * h];
@@ -598,11 +615,11 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 l_run[nt][i] = l_run[nt][i] * keep[nt][i] + sum;
             }
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    pf[nt][m][h] = transpose8x8(pack_f16x2(sc[nt][m][2 * h] * (m ? w1 : w0),
-                                                           sc[nt][m][2 * h + 1] * (m ? w1 : w0)));
+                    pf[nt][m][h] = transpose8x8(
+                        pack_f16x2(sc[nt][m][2 * h] * v_weight[m], sc[nt][m][2 * h + 1] * v_weight[m]));
         }
         if (__any_sync(0xffffffffu, moved)) {
             const float down = v_top / v_new;
@@ -621,7 +638,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         }
         // ---- O^T += V^T P^T ----------------------------------------------------------
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < M; ++m) {
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
 #pragma unroll
@@ -781,6 +798,7 @@ template <int D, int ROW>
 __global__ void __launch_bounds__(merge_warps(ROW) * 32)
     fa_decode_fp8_merge_kernel(const __grid_constant__ DecodeFp8 p, int slots) {
     constexpr int V = D / 32, kBatch = 8, kMergeWarps = merge_warps(ROW);
+    constexpr int TILE = tile_tokens(D);
     static_assert(kMergeWarps == ROW || ROW == 1, "a row's warps are the CTA's, or one");
     __shared__ float acc_sh[ROW][D], top_sh[ROW], sum_sh[ROW];
     const int lane = threadIdx.x & 31;
@@ -798,7 +816,7 @@ __global__ void __launch_bounds__(merge_warps(ROW) * 32)
         T = 0;
         Slice mine{};
         for (int first = 0; first < p.B; first += 32) {
-            const Slice s = of_lane(scan_lanes(p, first, pages, T), b % 32);
+            const Slice s = of_lane(scan_lanes<TILE>(p, first, pages, T), b % 32);
             if (first == b / 32 * 32) mine = s;
         }
         before = mine.tiles_before;
@@ -809,7 +827,7 @@ __global__ void __launch_bounds__(merge_warps(ROW) * 32)
         before = p.seqs[2 + 2 * static_cast<int64_t>(b)];
         len = static_cast<int>(p.seqs[3 + 2 * static_cast<int64_t>(b)]);
     }
-    const int n = tiles_of(len);
+    const int n = tiles_of<TILE>(len);
     const int hk = h / p.G, hg = h - hk * p.G, group = hg / p.group_heads;
     const int hh = hg - group * p.group_heads;
     T *= p.Hk;
@@ -922,7 +940,7 @@ Shape shape_of(int B, int H, int H_kv, int d, int num_sms) {
     s.groups = (G + 15) / 16;
     s.group_heads = (G + s.groups - 1) / s.groups;
     s.nt = s.group_heads > 8 ? 2 : 1;
-    s.ctas = num_sms * resident_ctas(d, s.nt);
+    s.ctas = num_sms * resident_ctas(s.nt);
     const int min_ctas = (s.groups + kWarps - 1) / kWarps;
     if (s.ctas < min_ctas) s.ctas = min_ctas;  // a warp for each group
     s.ranges = s.ctas * kWarps / s.groups;
@@ -979,7 +997,7 @@ int launch(const DecodeFp8& p, const Shape& s, cudaStream_t st) {
     const int64_t heads = static_cast<int64_t>(p.B) * p.Hk;
     const int64_t entries = p.max_pages ? static_cast<int64_t>(p.B) * p.max_pages : p.table_len;
     const int64_t pieces =
-        std::min<int64_t>(p.ranges, entries * (kPage / kTile) * p.Hk) / heads + 1;
+        std::min<int64_t>(p.ranges, entries * (kPage / tile_tokens(D)) * p.Hk) / heads + 1;
     const int each = pieces <= 8 ? 1 : pieces <= 48 ? 4 : 16;  // warps of a row
     const int64_t warps = static_cast<int64_t>(p.B) * p.H * each;
     cudaLaunchConfig_t cfg = {};
