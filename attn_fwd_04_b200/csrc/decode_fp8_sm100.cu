@@ -11,14 +11,15 @@
 // 关键术语解析, item 4.
 //
 // Two launches: split and merge.  The tokens of all sequences and K/V heads
-// form one stream of 32-token tiles (64 at d = 64), and each warp of a grid that fills the
+// form one stream of tiles of 32 tokens (64 at d = 64), and each warp of a grid that fills the
 // GPU takes an equal, contiguous piece of it, whatever the lengths.  A warp
 // that holds all of a sequence's head writes the output; pieces of one that is
 // cut are written as normalised partial outputs with their log-sum-exp, which
 // the second launch joins.  There is no plan kernel: each warp (each CTA, where
 // there are many sequences) sums the lengths itself while it starts.
 //
-// Within a warp nothing goes through shared memory but the query.  The matrix
+// With up to 8 query heads a K/V head nothing goes through shared memory but the
+// query (with more, tiles do: below).  The matrix
 // instruction's first operand is the cache: S^T[tokens, heads] = K Q^T and
 // O^T[d, heads] += V^T P^T, m16n8k16 in fp16 with fp32 sums, to which the
 // conversion from e4m3 is exact.  The order of d in the first product and of d
@@ -28,7 +29,7 @@
 // V's bytes are paired across two tokens (a byte permute).  S^T's accumulators
 // are P^T's operand after one 8 x 8 transpose in registers.  8 query heads
 // fill an instruction's 8 columns; up to 16 take two of them, more are split
-// into groups that neighbouring warps run side by side over the same tokens.
+// into groups, a warp each, over the same tokens.
 // (With the heads in the 16 rows instead, 8 heads would leave half of every
 // instruction and half of the accumulators empty.)
 //
@@ -290,10 +291,11 @@ __device__ __forceinline__ void enter_head(const DecodeFp8& p, Cursor& c) {
     c.ahead = k < (c.len - 1) / kPage ? page_index(p, c, k + 1) : 0;
 }
 
-template <int TILE>
+// The next tile; PAGES: and its page.
+template <int TILE, bool PAGES = true>
 __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
     if (++c.tile < c.tiles) {
-        if (c.tile % (kPage / TILE) == 0) {
+        if (PAGES && c.tile % (kPage / TILE) == 0) {
             c.slice = static_cast<int64_t>(c.ahead) * p.Hk + c.hk;
             const int k = c.tile / (kPage / TILE);
             c.ahead = k < (c.len - 1) / kPage ? page_index(p, c, k + 1) : 0;
@@ -311,7 +313,42 @@ __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
         } while (c.len == 0 && c.b + 1 < p.B);
         c.tiles = tiles_of<TILE>(c.len);
     }
-    enter_head<TILE>(p, c);
+    if (PAGES) enter_head<TILE>(p, c);
+}
+
+// ---- more than 8 query heads: tiles by way of shared memory --------------------------
+// A warp's accumulators then leave no registers for a tile on its way, and more
+// than 16 heads are two warps' work on the same bytes.  So a team of one or two
+// warps has a ring of tiles of its own, filled by asynchronous copies of 16 bytes,
+// all but one of its tiles ahead; with two, each copies half of a tile.  Where the
+// pieces go is permuted within 128-byte lines so that the 8 lanes of a phase of a
+// fragment's load find 8 different ones.
+//
+// 64 sequences of 8K to 16K tokens, 4 K/V heads of 16 query heads: 155 us, 0.84 of a
+// copy (tiles in registers 178; three tiles a ring leave room for one CTA an SM only:
+// 212).  Of 24 or 32: 265 us (each group of 16 by itself 330): both warps convert
+// every byte, and the products fill the warp-level pipe's better half.
+constexpr int ring_stages(int team) { return team == 1 ? 2 : 3; }
+constexpr int stage_bytes(int d) { return 2 * tile_tokens(d) * d + 128; }  // K, V, scales
+constexpr int ring_bytes(int d, int team) {
+    return kWarps / team * ring_stages(team) * stage_bytes(d);
+}
+
+template <int D>
+__device__ __forceinline__ int k_place(int row, int u) {  // of 16-byte piece u of a row
+    const int at = row * (D / 16) + u;
+    return D == 128 ? at ^ ((row & 1) << 2) : at;
+}
+template <int D>
+__device__ __forceinline__ int v_place(int row, int u) {
+    return (row * (D / 16) + u) ^ ((row >> 1 & 3) << 1);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // CTAs of four warps an SM, by their registers.
@@ -322,7 +359,8 @@ constexpr int resident_ctas(int nt) { return nt == 1 ? 3 : 2; }
 // of its tiles a warp, joins the warps' results in shared memory and writes the
 // output: one launch, and no length but its own sequence's (and those before it,
 // in a packed table).
-template <int D, int NT, int SOLO>
+// TEAM > 0: the warps that share a ring of tiles in shared memory.
+template <int D, int NT, int SOLO, int TEAM>
 __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                                   SOLO == 8 ? 1 : resident_ctas(NT))
     fa_decode_fp8_split_kernel(const __grid_constant__ DecodeFp8 p) {
@@ -330,6 +368,8 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
     constexpr int VW = D / 32;   // words of a token's V for each lane
     constexpr int MT = D / 16;   // 16-row tiles of O^T
     constexpr int TILE = tile_tokens(D), M = TILE / 16;
+    constexpr int kTeam = TEAM ? TEAM : 1, kStages = ring_stages(kTeam);
+    extern __shared__ uint4 ring[];
     __shared__ ScanShared scan;
     __shared__ Slice found[kWarps];
     __shared__ int found_b[kWarps];
@@ -363,8 +403,11 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
     } else {
     asm volatile("griddepcontrol.launch_dependents;");
     // consecutive ranges on different CTAs, so that a few spread over the SMs
-    wid = warp * gridDim.x + blockIdx.x;
-    const int r = wid / p.groups;
+    auto range_of_warp = [&](int w) {
+        return (w / kTeam * gridDim.x + blockIdx.x) / (p.groups / kTeam);
+    };
+    wid = (warp / kTeam * gridDim.x + blockIdx.x) * kTeam + warp % kTeam;
+    const int r = range_of_warp(warp);
     group = wid - r * p.groups;
     int64_t T, start;
     int ranges;
@@ -408,7 +451,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const int64_t at =
-                    range_start((w * gridDim.x + blockIdx.x) / p.groups, T, ranges);
+                    range_start(range_of_warp(w), T, ranges);
                 if (at >= s.tiles_before * p.Hk &&
                     at < (s.tiles_before + tiles_of<TILE>(s.len)) * p.Hk) {
                     found[w] = s;
@@ -464,6 +507,82 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         }
     };
 
+    // the same by way of the team's ring: tiles asked for, and taken, in turn
+    const int team = warp / kTeam;
+    const uint32_t stages = smem_u32(ring) + team * (kStages * stage_bytes(D));
+    Cursor asked = c;
+    int64_t to_ask = left;
+    int ask_at = 0, at = 0;
+    auto ask = [&]() {
+        if (to_ask > 0) {
+            const int slot0 = (asked.tile * TILE) % kPage;
+            const int last = slot0 + asked.len - 1 - asked.tile * TILE;
+            const uint32_t dst = stages + ask_at * stage_bytes(D);
+            const uint8_t* kb = p.kp + asked.slice * (kPage * D);
+            const uint8_t* vb = p.vp + asked.slice * (kPage * D);
+            const int me = warp % kTeam * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < TILE * D / 16 / (32 * kTeam); ++i) {
+                const int piece = i * 32 * kTeam + me, row = piece / (D / 16), u = piece % (D / 16);
+                const int off = min(slot0 + row, last) * D + 16 * u;
+                copy16(dst + 16 * k_place<D>(row, u), kb + off);
+                copy16(dst + TILE * D + 16 * v_place<D>(row, u), vb + off);
+            }
+            if (me < 2 * M) {
+                const int m = me % M;
+                copy4(dst + 2 * TILE * D + 4 * me,
+                      (me < M ? p.ks : p.vs) + (asked.slice << nb_log2) +
+                          (min(slot0 + 16 * m, last) >> p.block_log2));
+            }
+            if (--to_ask > 0) advance<TILE>(p, asked);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ask_at = ask_at + 1 == kStages ? 0 : ask_at + 1;
+    };
+    auto stage = [&]() {
+        return reinterpret_cast<const uint8_t*>(ring) +
+               (team * kStages + at) * stage_bytes(D);
+    };
+    auto take_k = [&]() {
+        const uint4* base = reinterpret_cast<const uint4*>(stage());
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            ks[m] = reinterpret_cast<const float*>(stage() + 2 * TILE * D)[m];
+            vs[m] = reinterpret_cast<const float*>(stage() + 2 * TILE * D)[M + m];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) {
+                    const uint4 x = base[k_place<D>(16 * m + 8 * h + g, t + 4 * j)];
+                    kr[m][h][j][0] = x.x;
+                    kr[m][h][j][1] = x.y;
+                    kr[m][h][j][2] = x.z;
+                    kr[m][h][j][3] = x.w;
+                }
+        }
+    };
+    auto take_v = [&]() {
+        const uint8_t* base = stage() + TILE * D;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 16 * m + 2 * t + (i & 1) + 8 * (i >> 1);
+                if constexpr (D == 128) {
+                    const uint4 x = reinterpret_cast<const uint4*>(base)[v_place<D>(row, g)];
+                    vr[m][i][0] = x.x;
+                    vr[m][i][1] = x.y;
+                    vr[m][i][2] = x.z;
+                    vr[m][i][3] = x.w;
+                } else {
+                    const uint2 x = *reinterpret_cast<const uint2*>(
+                        base + 16 * v_place<D>(row, g >> 1) + 8 * (g & 1));
+                    vr[m][i][0] = x.x;
+                    vr[m][i][1] = x.y;
+                }
+            }
+    };
+
     float o[NT][MT][4], m_run[NT][2], l_run[NT][2], fac[NT][2];
     float v_top = 0.f;  // power of two, at least every value scale so far
     // A new head of a sequence: its queries as fragments, and an empty state.
@@ -473,8 +592,8 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             const int hh = nt * 8 + g;
             const bool real = hh < heads;
             const __nv_bfloat16* row =
-                p.q + (static_cast<int64_t>(b) * p.H + hk * p.G + group * p.group_heads +
-                       (real ? hh : 0)) * D;
+                p.q + (static_cast<int64_t>(b) * p.H + hk * p.G +
+                       (real ? group * p.group_heads + hh : 0)) * D;
             float x[KJ][16], top = 0.f;
 #pragma unroll
             for (int j = 0; j < KJ; ++j) {
@@ -520,7 +639,10 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         v_top = 0x1p-64f;
     };
 
-    if (SOLO == 0 || left > 0) {
+    if constexpr (TEAM > 0) {
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) ask();
+    } else if (SOLO == 0 || left > 0) {
         load_k(c);
         load_v(c);
     }
@@ -531,7 +653,16 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         const int b = c.b, hk = c.hk, tok0 = c.tile * TILE, len = c.len;
         const bool seg_end = c.tile + 1 == c.tiles, more = left > 1;
         --left;
-        if (more) advance<TILE>(p, c);
+        if (more) advance<TILE, TEAM == 0>(p, c);
+        if constexpr (TEAM > 0) {
+            // this thread's copies of the tile are there; so are the team's, and the
+            // team is done with the tile before it
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();
+            if (TEAM > 1) bar_sync_named(1 + team, TEAM * 32);
+            ask();
+            take_k();
+        }
         // ---- S^T = K Q^T -------------------------------------------------------
         float sc[NT][M][4];
 #pragma unroll
@@ -570,7 +701,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             v_weight[m] = vs[m];
             v_most = max(v_most, __float_as_uint(vs[m]));
         }
-        if (more) load_k(c);
+        if (TEAM == 0 && more) load_k(c);
         // ---- softmax over the tile's tokens ---------------------------------------
         const float v_new = fmaxf(
             v_top, __uint_as_float((v_most + 0x7fffffu) & 0x7f800000u));
@@ -636,6 +767,10 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             }
             v_top = v_new;
         }
+        if constexpr (TEAM > 0) {
+            take_v();
+            at = at + 1 == kStages ? 0 : at + 1;
+        }
         // ---- O^T += V^T P^T ----------------------------------------------------------
 #pragma unroll
         for (int m = 0; m < M; ++m) {
@@ -652,7 +787,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 }
             }
         }
-        if (more) load_v(c);
+        if (TEAM == 0 && more) load_v(c);
         if (SOLO > 0 || (!seg_end && more)) continue;
         // ---- the end of a head, or of the warp's range ------------------------------
         whole = whole && seg_end;
@@ -930,7 +1065,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 // How the query heads of a K/V head and the warps are cut.
 struct Shape {
-    int groups, group_heads, nt, ctas, ranges;
+    int groups, group_heads, nt, team, ctas, ranges;
     size_t seqs_bytes, lse_bytes, bytes;  // of the workspace: sequences, sums, pieces
 };
 
@@ -938,12 +1073,15 @@ Shape shape_of(int B, int H, int H_kv, int d, int num_sms) {
     Shape s;
     const int G = H / H_kv;
     s.groups = (G + 15) / 16;
+    s.groups += s.groups > 1 && s.groups % 2 != 0;  // two warps' work at a time
     s.group_heads = (G + s.groups - 1) / s.groups;
     s.nt = s.group_heads > 8 ? 2 : 1;
+    s.team = s.nt == 1 ? 0 : s.groups > 1 ? 2 : 1;
     s.ctas = num_sms * resident_ctas(s.nt);
     const int min_ctas = (s.groups + kWarps - 1) / kWarps;
     if (s.ctas < min_ctas) s.ctas = min_ctas;  // a warp for each group
-    s.ranges = s.ctas * kWarps / s.groups;
+    const int teams = s.team ? s.team : 1;
+    s.ranges = s.ctas * (kWarps / teams) / (s.groups / teams);
     const size_t rows = static_cast<size_t>(s.ctas) * kWarps * 2 * 8 * s.nt;
     s.lse_bytes = (rows * sizeof(float) + 255) & ~size_t{255};
     s.seqs_bytes = B > kWarpSeqs ? ((2 + 2 * static_cast<size_t>(B)) * 8 + 255) & ~size_t{255} : 0;
@@ -979,16 +1117,22 @@ int launch_solo(DecodeFp8& p, const Shape& s, int num_sms, cudaStream_t st) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    auto kernel = s.nt == 2 ? fa_decode_fp8_split_kernel<D, 2, 4>
-                  : wide    ? fa_decode_fp8_split_kernel<D, 1, 8>
-                            : fa_decode_fp8_split_kernel<D, 1, 4>;
+    auto kernel = s.nt == 2 ? fa_decode_fp8_split_kernel<D, 2, 4, 0>
+                  : wide    ? fa_decode_fp8_split_kernel<D, 1, 8, 0>
+                            : fa_decode_fp8_split_kernel<D, 1, 4, 0>;
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D>
 int launch(const DecodeFp8& p, const Shape& s, cudaStream_t st) {
-    if (s.nt == 1) fa_decode_fp8_split_kernel<D, 1, 0><<<s.ctas, kThreads, 0, st>>>(p);
-    else fa_decode_fp8_split_kernel<D, 2, 0><<<s.ctas, kThreads, 0, st>>>(p);
+    auto split = s.team == 0   ? fa_decode_fp8_split_kernel<D, 1, 0, 0>
+                 : s.team == 1 ? fa_decode_fp8_split_kernel<D, 2, 0, 1>
+                               : fa_decode_fp8_split_kernel<D, 2, 0, 2>;
+    const int ring = s.team ? ring_bytes(D, s.team) : 0;
+    if (ring && cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, ring) !=
+                    cudaSuccess)
+        return FA_ERR_CUDA;
+    split<<<s.ctas, kThreads, ring, st>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     // Pieces of a head, at most on average: the ranges, or the tiles that the table
     // has room for.  Rows of a few pieces take a warp each (2048 rows of 4: 18.4 us

@@ -112,11 +112,20 @@ def test_decode(table, lens, H, Hk, d, block):
     c.both()
 
 
-@pytest.mark.parametrize("G", [3, 9, 11, 12, 16, 17, 24, 32, 33, 48])
+@pytest.mark.parametrize("G", [3, 9, 11, 12, 16, 17, 24, 32, 33, 48, 272])
 @pytest.mark.parametrize("d", [64, 128])
 def test_group_sizes(G, d):
     c = Cache([300, 0, 1, 1025], 2 * G, 2, d, 64, "rows", seed=G)
     c.both()
+
+
+@pytest.mark.parametrize("G", [12, 32, 40])
+@pytest.mark.parametrize("d,block", [(64, 16), (128, 32), (64, 128)])
+def test_wide_groups_over_long_and_many_sequences(G, d, block):
+    for lens, Hk, table in (([9000, 1, 0, 2500], 1, "packed"),
+                            ([(i * 61) % 700 for i in range(150)], 2, "rows")):
+        c = Cache(lens, G * Hk, Hk, d, block, table, seed=G, spread=4.0)
+        c.both()
 
 
 def test_long_sequences_beside_short_ones():
