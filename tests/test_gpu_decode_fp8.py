@@ -420,3 +420,76 @@ def test_the_binding_s_two_ways_agree():
         for stream in (None, here):
             with pytest.raises((fa.FaError, ValueError)):
                 fa.fa_qk_norm_rope(q, k, rope_cos=cos, rope_sin=sin, stream=stream, **bad)
+
+
+def test_a_decode_step_captured_once_and_replayed():
+    """Append and decode in one graph, the lengths counted on the device, over the
+    borders of blocks and pages: the same bits as the calls made one by one."""
+    H, Hk, d, block, B = 8, 2, 128, 16, 3
+    g = torch.Generator().manual_seed(4)
+    cos, sin = fa.fa_rope_table(1024, d)
+    w = 1 + 0.2 * torch.randn(d, generator=g).cuda()
+    rows = torch.randperm(4 * B, generator=g).int().view(B, 4).cuda()
+    cu = torch.arange(B + 1).int().cuda()
+    prompt = torch.randn((3 * 14, (H + 2 * Hk) * d), generator=g).bfloat16().cuda()
+
+    def parts(x):
+        return [t.view(len(x), -1, d) for t in x.split([H * d, Hk * d, Hk * d], 1)]
+
+    class State:
+        def __init__(self):
+            self.kp, self.vp = (torch.zeros((4 * B, Hk, PS, d), device="cuda").to(FP8)
+                                for _ in range(2))
+            self.ks, self.vs = (torch.ones((4 * B, Hk, PS // block), device="cuda")
+                                for _ in range(2))
+            self.seq = torch.tensor([14, 250, 14]).int().cuda()
+            self.x = torch.zeros((B, prompt.shape[1]), device="cuda").bfloat16()
+            first = torch.tensor([0, 14, 28, 42]).int().cuda()
+            fa.fa_append_paged_fp8(*parts(prompt), first, self.kp, self.vp, self.ks, self.vs,
+                                   rows, self.seq, cos, sin, w, w)
+
+        def step(self):
+            self.seq += 1
+            q = fa.fa_append_paged_fp8(*parts(self.x), cu, self.kp, self.vp, self.ks, self.vs,
+                                       rows, self.seq, cos, sin, w, w)
+            return fa.fa_decode_paged_fp8(q, self.kp, self.vp, self.ks, self.vs, rows, self.seq)
+
+    # (the second sequence's earlier tokens are zeros: never written)
+    a, b = State(), State()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = a.step()
+    for i in range(12):
+        x = (torch.randn(a.x.shape, generator=g) * 2.0 ** (i % 5 - 2)).bfloat16().cuda()
+        a.x.copy_(x)
+        b.x.copy_(x)
+        graph.replay()
+        assert torch.equal(out, b.step()), i
+    _ok()
+    for n in ("kp", "vp", "ks", "vs"):
+        assert torch.equal(getattr(a, n).view(torch.uint8), getattr(b, n).view(torch.uint8))
+
+
+def test_library_workspaces_of_two_streams():
+    """Calls on the current stream take the library's workspace of that stream."""
+    a = Cache([9000, 20, 3000], 8, 2, 128, 64, "packed", seed=7)
+    b = Cache([5000, 7000, 1], 24, 1, 64, 32, "rows", seed=8)
+    tables = [a.table.cuda(), b.table.cuda()]
+
+    def call(c, t):
+        return fa.fa_decode_paged_fp8(c.q, c.kp, c.vp, c.ks, c.vs, t, c.seq)
+
+    want = [call(a, tables[0]), call(b, tables[1])]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(40):
+        for i, (c, s) in enumerate(zip((a, b), streams)):
+            with torch.cuda.stream(s):
+                got[i].append(call(c, tables[i]))
+    torch.cuda.synchronize()
+    _ok()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, x) for x in g)
