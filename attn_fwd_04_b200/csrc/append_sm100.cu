@@ -270,7 +270,8 @@ __device__ __forceinline__ void append_rows(const Append& p, int cta, Shared& sh
 }
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 3) fa_append_rope_kernel(const __grid_constant__ Append p) {
+__global__ void __launch_bounds__(kThreads, 3)
+    fa_append_rope_kernel(const __grid_constant__ Append p) {
     __shared__ Shared sh;
     append_rows<D, INTER, true>(p, blockIdx.x, sh);
 }
@@ -594,7 +595,8 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
     float* scale = (is_k ? p.ks : p.vs) + (b.slice0 + h_begin + part) * per_page +
                    (b.at >> p.block_log2);
     uint8_t* const codes = static_cast<uint8_t*>(is_k ? p.kp : p.vp);
-    uint8_t* dst = codes + ((b.slice0 + h_begin + part) * kPage + b.at + (b.first - b.lo) + tok) * D;
+    uint8_t* dst =
+        codes + ((b.slice0 + h_begin + part) * kPage + b.at + (b.first - b.lo) + tok) * D;
     aim(0, h_begin + part);
     place(0);
 #pragma unroll

@@ -411,8 +411,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         need(shaped(lens, ScalarType::Int, {B}));
         const int32_t* len_p = lens.const_data_ptr<int32_t>();
         const Table table(a[5], B, len_p);
-        const float scale =
-            static_cast<float>(a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[8]));
+        const float scale = static_cast<float>(
+            a[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(d)) : number(a[8]));
         Tensor o;
         if (a[9] == Py_None) {
             o = bf16_like(q);
@@ -420,8 +420,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
             o = tensor(a[9]);
             need(shaped(o, ScalarType::BFloat16, q.sizes()));
         }
-        float* lse =
-            const_cast<float*>(static_cast<const float*>(optional(a[10], ScalarType::Float, {B, H})));
+        float* lse = const_cast<float*>(
+            static_cast<const float*>(optional(a[10], ScalarType::Float, {B, H})));
         const auto run = [&](void* ws, int bytes) {
             return g_fa.decode(q.const_data_ptr(), pool.k.const_data_ptr(),
                                pool.v.const_data_ptr(), s.k.const_data_ptr<float>(),

@@ -317,22 +317,20 @@ __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
 }
 
 // ---- more than 8 query heads: tiles by way of shared memory --------------------------
-// A warp's accumulators then leave no registers for a tile on its way, and more
-// than 16 heads are two warps' work on the same bytes.  So a team of one or two
-// warps has a ring of tiles of its own, filled by asynchronous copies of 16 bytes,
-// all but one of its tiles ahead; with two, each copies half of a tile.  Where the
-// pieces go is permuted within 128-byte lines so that the 8 lanes of a phase of a
-// fragment's load find 8 different ones.
+// A warp's accumulators (16 registers for every 8 heads, at d = 128 32) then leave no
+// room for a tile on its way, so each warp has a ring of two tiles of its own,
+// filled by asynchronous copies of 16 bytes one tile ahead.  Where the pieces go is
+// permuted within 128-byte lines so that the 8 lanes of a phase of a fragment's load
+// find 8 different ones.  Up to 32 heads share a warp, and so one conversion of the
+// tile's bytes.
 //
-// 64 sequences of 8K to 16K tokens, 4 K/V heads of 16 query heads: 155 us, 0.84 of a
-// copy (tiles in registers 178; three tiles a ring leave room for one CTA an SM only:
-// 212).  Of 24 or 32: 265 us (each group of 16 by itself 330): both warps convert
-// every byte, and the products fill the warp-level pipe's better half.
-constexpr int ring_stages(int team) { return team == 1 ? 2 : 3; }
+// 64 sequences of 8K to 16K tokens, 4 K/V heads of 16 query heads: 154 us, 0.84 of a
+// copy (tiles in registers 178); of 24 197 and of 32 258 (as groups of 12 and of 16,
+// side by side on the same bytes, 264 and 266): the products bound them, some 64 us
+// for every 8 heads.
+constexpr int kStages = 2;  // (three leave room for one CTA an SM only)
 constexpr int stage_bytes(int d) { return 2 * tile_tokens(d) * d + 128; }  // K, V, scales
-constexpr int ring_bytes(int d, int team) {
-    return kWarps / team * ring_stages(team) * stage_bytes(d);
-}
+constexpr int ring_bytes(int d) { return kWarps * kStages * stage_bytes(d); }
 
 template <int D>
 __device__ __forceinline__ int k_place(int row, int u) {  // of 16-byte piece u of a row
@@ -359,8 +357,8 @@ constexpr int resident_ctas(int nt) { return nt == 1 ? 3 : 2; }
 // of its tiles a warp, joins the warps' results in shared memory and writes the
 // output: one launch, and no length but its own sequence's (and those before it,
 // in a packed table).
-// TEAM > 0: the warps that share a ring of tiles in shared memory.
-template <int D, int NT, int SOLO, int TEAM>
+// RING: tiles by way of shared memory.
+template <int D, int NT, int SOLO, bool RING>
 __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                                   SOLO == 8 ? 1 : resident_ctas(NT))
     fa_decode_fp8_split_kernel(const __grid_constant__ DecodeFp8 p) {
@@ -368,7 +366,6 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
     constexpr int VW = D / 32;   // words of a token's V for each lane
     constexpr int MT = D / 16;   // 16-row tiles of O^T
     constexpr int TILE = tile_tokens(D), M = TILE / 16;
-    constexpr int kTeam = TEAM ? TEAM : 1, kStages = ring_stages(kTeam);
     extern __shared__ uint4 ring[];
     __shared__ ScanShared scan;
     __shared__ Slice found[kWarps];
@@ -403,11 +400,8 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
     } else {
     asm volatile("griddepcontrol.launch_dependents;");
     // consecutive ranges on different CTAs, so that a few spread over the SMs
-    auto range_of_warp = [&](int w) {
-        return (w / kTeam * gridDim.x + blockIdx.x) / (p.groups / kTeam);
-    };
-    wid = (warp / kTeam * gridDim.x + blockIdx.x) * kTeam + warp % kTeam;
-    const int r = range_of_warp(warp);
+    wid = warp * gridDim.x + blockIdx.x;
+    const int r = wid / p.groups;
     group = wid - r * p.groups;
     int64_t T, start;
     int ranges;
@@ -451,7 +445,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const int64_t at =
-                    range_start(range_of_warp(w), T, ranges);
+                    range_start((w * gridDim.x + blockIdx.x) / p.groups, T, ranges);
                 if (at >= s.tiles_before * p.Hk &&
                     at < (s.tiles_before + tiles_of<TILE>(s.len)) * p.Hk) {
                     found[w] = s;
@@ -477,20 +471,21 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
 
     const int heads = min(p.group_heads, p.G - group * p.group_heads);  // of this group
     const int nb_log2 = 8 - p.block_log2;  // blocks of a page
-    uint32_t kr[M][2][KJ][4], vr[M][4][VW];
+    uint32_t kr[M][2][RING ? 1 : KJ][4], vr[RING ? 1 : M][4][VW];  // (a ring's part by part)
     float ks[M], vs[M];
     auto load_k = [&](const Cursor& x) {
         const int slot0 = (x.tile * TILE) % kPage, last = slot0 + x.len - 1 - x.tile * TILE;
         const uint8_t* base = p.kp + x.slice * (kPage * D) + 16 * t;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            ks[m] = __ldg(p.ks + (x.slice << nb_log2) + (min(slot0 + 16 * m, last) >> p.block_log2));
+            ks[m] = __ldg(p.ks + (x.slice << nb_log2) +
+                          (min(slot0 + 16 * m, last) >> p.block_log2));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 // behind the last token: that token again
                 const uint8_t* row = base + min(slot0 + 16 * m + 8 * h + g, last) * D;
 #pragma unroll
-                for (int j = 0; j < KJ; ++j) load_bytes(kr[m][h][j], row + 64 * j);
+                for (int j = 0; j < KJ; ++j) load_bytes(kr[m][h][RING ? 0 : j], row + 64 * j);
             }
         }
     };
@@ -499,17 +494,17 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         const uint8_t* base = p.vp + x.slice * (kPage * D) + D / 8 * g;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            vs[m] = __ldg(p.vs + (x.slice << nb_log2) + (min(slot0 + 16 * m, last) >> p.block_log2));
+            vs[m] = __ldg(p.vs + (x.slice << nb_log2) +
+                          (min(slot0 + 16 * m, last) >> p.block_log2));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                load_bytes(vr[m][i],
+                load_bytes(vr[RING ? 0 : m][i],
                            base + min(slot0 + 16 * m + 2 * t + (i & 1) + 8 * (i >> 1), last) * D);
         }
     };
 
-    // the same by way of the team's ring: tiles asked for, and taken, in turn
-    const int team = warp / kTeam;
-    const uint32_t stages = smem_u32(ring) + team * (kStages * stage_bytes(D));
+    // the same by way of the ring: tiles asked for, and taken, in turn
+    const uint32_t stages = smem_u32(ring) + warp * (kStages * stage_bytes(D));
     Cursor asked = c;
     int64_t to_ask = left;
     int ask_at = 0, at = 0;
@@ -520,67 +515,58 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             const uint32_t dst = stages + ask_at * stage_bytes(D);
             const uint8_t* kb = p.kp + asked.slice * (kPage * D);
             const uint8_t* vb = p.vp + asked.slice * (kPage * D);
-            const int me = warp % kTeam * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < TILE * D / 16 / (32 * kTeam); ++i) {
-                const int piece = i * 32 * kTeam + me, row = piece / (D / 16), u = piece % (D / 16);
+            for (int i = 0; i < TILE * D / 16 / 32; ++i) {
+                const int piece = i * 32 + lane, row = piece / (D / 16), u = piece % (D / 16);
                 const int off = min(slot0 + row, last) * D + 16 * u;
                 copy16(dst + 16 * k_place<D>(row, u), kb + off);
                 copy16(dst + TILE * D + 16 * v_place<D>(row, u), vb + off);
             }
-            if (me < 2 * M) {
-                const int m = me % M;
-                copy4(dst + 2 * TILE * D + 4 * me,
-                      (me < M ? p.ks : p.vs) + (asked.slice << nb_log2) +
+            if (lane < 2 * M) {
+                const int m = lane % M;
+                copy4(dst + 2 * TILE * D + 4 * lane,
+                      (lane < M ? p.ks : p.vs) + (asked.slice << nb_log2) +
                           (min(slot0 + 16 * m, last) >> p.block_log2));
             }
             if (--to_ask > 0) advance<TILE>(p, asked);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
-        ask_at = ask_at + 1 == kStages ? 0 : ask_at + 1;
+        ask_at ^= 1;
     };
     auto stage = [&]() {
-        return reinterpret_cast<const uint8_t*>(ring) +
-               (team * kStages + at) * stage_bytes(D);
+        return reinterpret_cast<const uint8_t*>(ring) + (warp * kStages + at) * stage_bytes(D);
     };
-    auto take_k = [&]() {
+    auto take_k = [&](int j) {  // the tokens' 64 values from 64 j on
         const uint4* base = reinterpret_cast<const uint4*>(stage());
-#pragma unroll
-        for (int m = 0; m < M; ++m) {
-            ks[m] = reinterpret_cast<const float*>(stage() + 2 * TILE * D)[m];
-            vs[m] = reinterpret_cast<const float*>(stage() + 2 * TILE * D)[M + m];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < KJ; ++j) {
-                    const uint4 x = base[k_place<D>(16 * m + 8 * h + g, t + 4 * j)];
-                    kr[m][h][j][0] = x.x;
-                    kr[m][h][j][1] = x.y;
-                    kr[m][h][j][2] = x.z;
-                    kr[m][h][j][3] = x.w;
-                }
-        }
-    };
-    auto take_v = [&]() {
-        const uint8_t* base = stage() + TILE * D;
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 16 * m + 2 * t + (i & 1) + 8 * (i >> 1);
-                if constexpr (D == 128) {
-                    const uint4 x = reinterpret_cast<const uint4*>(base)[v_place<D>(row, g)];
-                    vr[m][i][0] = x.x;
-                    vr[m][i][1] = x.y;
-                    vr[m][i][2] = x.z;
-                    vr[m][i][3] = x.w;
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2*>(
-                        base + 16 * v_place<D>(row, g >> 1) + 8 * (g & 1));
-                    vr[m][i][0] = x.x;
-                    vr[m][i][1] = x.y;
-                }
+            for (int h = 0; h < 2; ++h) {
+                const uint4 x = base[k_place<D>(16 * m + 8 * h + g, t + 4 * j)];
+                kr[m][h][0][0] = x.x;
+                kr[m][h][0][1] = x.y;
+                kr[m][h][0][2] = x.z;
+                kr[m][h][0][3] = x.w;
             }
+    };
+    auto take_v = [&](int m) {  // of 16 tokens
+        const uint8_t* base = stage() + TILE * D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 16 * m + 2 * t + (i & 1) + 8 * (i >> 1);
+            if constexpr (D == 128) {
+                const uint4 x = reinterpret_cast<const uint4*>(base)[v_place<D>(row, g)];
+                vr[0][i][0] = x.x;
+                vr[0][i][1] = x.y;
+                vr[0][i][2] = x.z;
+                vr[0][i][3] = x.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(
+                    base + 16 * v_place<D>(row, g >> 1) + 8 * (g & 1));
+                vr[0][i][0] = x.x;
+                vr[0][i][1] = x.y;
+            }
+        }
     };
 
     float o[NT][MT][4], m_run[NT][2], l_run[NT][2], fac[NT][2];
@@ -639,9 +625,8 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         v_top = 0x1p-64f;
     };
 
-    if constexpr (TEAM > 0) {
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) ask();
+    if constexpr (RING) {
+        ask();
     } else if (SOLO == 0 || left > 0) {
         load_k(c);
         load_v(c);
@@ -653,15 +638,17 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         const int b = c.b, hk = c.hk, tok0 = c.tile * TILE, len = c.len;
         const bool seg_end = c.tile + 1 == c.tiles, more = left > 1;
         --left;
-        if (more) advance<TILE, TEAM == 0>(p, c);
-        if constexpr (TEAM > 0) {
-            // this thread's copies of the tile are there; so are the team's, and the
-            // team is done with the tile before it
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        if (more) advance<TILE, !RING>(p, c);
+        if constexpr (RING) {
+            // the tile's copies, by all lanes, are there; all are done with the one before
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
             __syncwarp();
-            if (TEAM > 1) bar_sync_named(1 + team, TEAM * 32);
             ask();
-            take_k();
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                ks[m] = reinterpret_cast<const float*>(stage() + 2 * TILE * D)[m];
+                vs[m] = reinterpret_cast<const float*>(stage() + 2 * TILE * D)[M + m];
+            }
         }
         // ---- S^T = K Q^T -------------------------------------------------------
         float sc[NT][M][4];
@@ -673,6 +660,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 for (int i = 0; i < 4; ++i) sc[nt][m][i] = 0.f;
 #pragma unroll
         for (int j = 0; j < KJ; ++j) {
+            if (RING) take_k(j);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint4 qf[NT];
@@ -683,8 +671,8 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
                         uint32_t a0, a1, a2, a3;
-                        cvt4(kr[m][0][j][2 * h + s2], a0, a2);
-                        cvt4(kr[m][1][j][2 * h + s2], a1, a3);
+                        cvt4(kr[m][0][RING ? 0 : j][2 * h + s2], a0, a2);
+                        cvt4(kr[m][1][RING ? 0 : j][2 * h + s2], a1, a3);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma_f16(sc[nt][m], a0, a1, a2, a3, s2 ? qf[nt].z : qf[nt].x,
@@ -701,7 +689,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             v_weight[m] = vs[m];
             v_most = max(v_most, __float_as_uint(vs[m]));
         }
-        if (TEAM == 0 && more) load_k(c);
+        if (!RING && more) load_k(c);
         // ---- softmax over the tile's tokens ---------------------------------------
         const float v_new = fmaxf(
             v_top, __uint_as_float((v_most + 0x7fffffu) & 0x7f800000u));
@@ -749,8 +737,8 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    pf[nt][m][h] = transpose8x8(
-                        pack_f16x2(sc[nt][m][2 * h] * v_weight[m], sc[nt][m][2 * h + 1] * v_weight[m]));
+                    pf[nt][m][h] = transpose8x8(pack_f16x2(sc[nt][m][2 * h] * v_weight[m],
+                                                           sc[nt][m][2 * h + 1] * v_weight[m]));
         }
         if (__any_sync(0xffffffffu, moved)) {
             const float down = v_top / v_new;
@@ -767,27 +755,26 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             }
             v_top = v_new;
         }
-        if constexpr (TEAM > 0) {
-            take_v();
-            at = at + 1 == kStages ? 0 : at + 1;
-        }
         // ---- O^T += V^T P^T ----------------------------------------------------------
 #pragma unroll
         for (int m = 0; m < M; ++m) {
+            if (RING) take_v(m);
+            const int from = RING ? 0 : m;
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
 #pragma unroll
                 for (int hi = 0; hi < 2; ++hi) {
                     uint32_t a0, a1, a2, a3;
-                    cvt4(__byte_perm(vr[m][0][w], vr[m][1][w], hi ? 0x7362 : 0x5140), a0, a1);
-                    cvt4(__byte_perm(vr[m][2][w], vr[m][3][w], hi ? 0x7362 : 0x5140), a2, a3);
+                    cvt4(__byte_perm(vr[from][0][w], vr[from][1][w], hi ? 0x7362 : 0x5140), a0, a1);
+                    cvt4(__byte_perm(vr[from][2][w], vr[from][3][w], hi ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         mma_f16(o[nt][2 * w + hi], a0, a1, a2, a3, pf[nt][m][0], pf[nt][m][1]);
                 }
             }
         }
-        if (TEAM == 0 && more) load_v(c);
+        if (RING) at ^= 1;
+        if (!RING && more) load_v(c);
         if (SOLO > 0 || (!seg_end && more)) continue;
         // ---- the end of a head, or of the warp's range ------------------------------
         whole = whole && seg_end;
@@ -1063,30 +1050,44 @@ __global__ void __launch_bounds__(merge_warps(ROW) * 32)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// How the query heads of a K/V head and the warps are cut.
+// How the query heads of a K/V head and the warps are cut: up to kMostHeads of them
+// to a warp, kFewHeads where the stream is short or a sequence's head has CTAs of its
+// own, and more warps are worth more than fewer products and conversions.
+constexpr int kMostHeads = 32, kFewHeads = 16;
 struct Shape {
-    int groups, group_heads, nt, team, ctas, ranges;
+    int groups, group_heads, nt, ctas, ranges;
     size_t seqs_bytes, lse_bytes, bytes;  // of the workspace: sequences, sums, pieces
 };
 
-Shape shape_of(int B, int H, int H_kv, int d, int num_sms) {
+// (most: query heads of a group)
+Shape shape_of(int B, int H, int H_kv, int d, int num_sms, int most) {
     Shape s;
     const int G = H / H_kv;
-    s.groups = (G + 15) / 16;
-    s.groups += s.groups > 1 && s.groups % 2 != 0;  // two warps' work at a time
+    s.groups = (G + most - 1) / most;
     s.group_heads = (G + s.groups - 1) / s.groups;
-    s.nt = s.group_heads > 8 ? 2 : 1;
-    s.team = s.nt == 1 ? 0 : s.groups > 1 ? 2 : 1;
+    s.nt = (s.group_heads + 7) / 8;
     s.ctas = num_sms * resident_ctas(s.nt);
     const int min_ctas = (s.groups + kWarps - 1) / kWarps;
     if (s.ctas < min_ctas) s.ctas = min_ctas;  // a warp for each group
-    const int teams = s.team ? s.team : 1;
-    s.ranges = s.ctas * (kWarps / teams) / (s.groups / teams);
+    s.ranges = s.ctas * kWarps / s.groups;
     const size_t rows = static_cast<size_t>(s.ctas) * kWarps * 2 * 8 * s.nt;
     s.lse_bytes = (rows * sizeof(float) + 255) & ~size_t{255};
     s.seqs_bytes = B > kWarpSeqs ? ((2 + 2 * static_cast<size_t>(B)) * 8 + 255) & ~size_t{255} : 0;
     s.bytes = s.seqs_bytes + s.lse_bytes + rows * d * sizeof(float);
     return s;
+}
+
+// Scratch of a call, whichever way it takes.
+size_t scratch_bytes(int B, int H, int H_kv, int d, int num_sms) {
+    return std::max(shape_of(B, H, H_kv, d, num_sms, kFewHeads).bytes,
+                    shape_of(B, H, H_kv, d, num_sms, kMostHeads).bytes);
+}
+
+// Up to four tiles a warp, as far as the table tells (one sequence of 32K tokens with
+// one K/V head of 32: 16 us in groups of 16 heads, 25 in one of 32).
+bool is_short(const Shape& s, int B, int H_kv, int d, int max_pages, int table_len) {
+    const int64_t entries = max_pages ? static_cast<int64_t>(B) * max_pages : table_len;
+    return entries * (kPage / tile_tokens(d)) * H_kv <= 4 * static_cast<int64_t>(s.ranges);
 }
 
 // CTAs of its own for each sequence's head, where a table row holds a few pages (a
@@ -1117,18 +1118,19 @@ int launch_solo(DecodeFp8& p, const Shape& s, int num_sms, cudaStream_t st) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = p.cluster > 1 ? 1 : 0;
-    auto kernel = s.nt == 2 ? fa_decode_fp8_split_kernel<D, 2, 4, 0>
-                  : wide    ? fa_decode_fp8_split_kernel<D, 1, 8, 0>
-                            : fa_decode_fp8_split_kernel<D, 1, 4, 0>;
+    auto kernel = s.nt == 2 ? fa_decode_fp8_split_kernel<D, 2, 4, false>
+                  : wide    ? fa_decode_fp8_split_kernel<D, 1, 8, false>
+                            : fa_decode_fp8_split_kernel<D, 1, 4, false>;
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D>
 int launch(const DecodeFp8& p, const Shape& s, cudaStream_t st) {
-    auto split = s.team == 0   ? fa_decode_fp8_split_kernel<D, 1, 0, 0>
-                 : s.team == 1 ? fa_decode_fp8_split_kernel<D, 2, 0, 1>
-                               : fa_decode_fp8_split_kernel<D, 2, 0, 2>;
-    const int ring = s.team ? ring_bytes(D, s.team) : 0;
+    auto split = s.nt == 1   ? fa_decode_fp8_split_kernel<D, 1, 0, false>
+                 : s.nt == 2 ? fa_decode_fp8_split_kernel<D, 2, 0, true>
+                 : s.nt == 3 ? fa_decode_fp8_split_kernel<D, 3, 0, true>
+                             : fa_decode_fp8_split_kernel<D, 4, 0, true>;
+    const int ring = s.nt > 1 ? ring_bytes(D) : 0;
     if (ring && cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, ring) !=
                     cudaSuccess)
         return FA_ERR_CUDA;
@@ -1172,9 +1174,9 @@ int fa_decode_paged_fp8_workspace(int B, int H, int H_kv, int d, int* bytes) {
     unsigned int* err = nullptr;
     int num_sms = 0, rc;
     if ((rc = fa::device_error_word(&err, &num_sms)) != FA_OK) return rc;
-    const fa::Shape s = fa::shape_of(B, H, H_kv, d, num_sms);
-    if (s.bytes > 0x7fffffff) return FA_ERR_SHAPE;
-    *bytes = static_cast<int>(s.bytes);
+    const size_t most = fa::scratch_bytes(B, H, H_kv, d, num_sms);
+    if (most > 0x7fffffff) return FA_ERR_SHAPE;
+    *bytes = static_cast<int>(most);
     return FA_OK;
 }
 
@@ -1207,18 +1209,21 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
     fa::DecodeFp8 p{};
     int num_sms = 0, rc;
     if ((rc = fa::device_error_word(&p.err, &num_sms)) != FA_OK) return rc;
-    const fa::Shape s = fa::shape_of(B, H, H_kv, d, num_sms);
-    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    const bool solo = fa::is_solo(static_cast<int64_t>(B) * H_kv * s.groups, max_pages, table_len,
+    const fa::Shape few = fa::shape_of(B, H, H_kv, d, num_sms, fa::kFewHeads);
+    const fa::Shape most = fa::shape_of(B, H, H_kv, d, num_sms, fa::kMostHeads);
+    const bool solo = fa::is_solo(static_cast<int64_t>(B) * H_kv * few.groups, max_pages, table_len,
                                   num_sms);
+    const fa::Shape& s =
+        solo || fa::is_short(few, B, H_kv, d, max_pages, table_len) ? few : most;
+    const size_t need = fa::scratch_bytes(B, H, H_kv, d, num_sms);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!solo) {
         void* ws = nullptr;
-        if ((rc = fa::call_workspace(workspace, workspace_bytes, s.bytes, st, &ws)) != FA_OK)
-            return rc;
+        if ((rc = fa::call_workspace(workspace, workspace_bytes, need, st, &ws)) != FA_OK) return rc;
         p.seqs = static_cast<int64_t*>(ws);
         p.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + s.seqs_bytes);
         p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + s.seqs_bytes + s.lse_bytes);
-    } else if (workspace && static_cast<size_t>(workspace_bytes) < s.bytes) {
+    } else if (workspace && static_cast<size_t>(workspace_bytes) < need) {
         return FA_ERR_SHAPE;  // as for any other table
     }
     p.q = static_cast<const __nv_bfloat16*>(q);

@@ -14,7 +14,8 @@
 // values of the halves layout in a lane, the exchange was 8 shuffles a row and
 // the table's reads twice as many: 88 us instead of 69 for 16384 tokens of 40
 // heads.)  Values are held in pairs for the instructions that take two at a time,
-// which with slots found without a division made that 60.  R is a multiple of 16, so the 4 lie in one half.  The rotation
+// which with slots found without a division made that 60.  R is a multiple of 16,
+// so the 4 lie in one half.  The rotation
 // rounds each product and then their sum (no fused multiply-add): the same
 // rounding as the rotation inside fa_fwd_rope, so that the two agree bit for
 // bit where there is no norm.

@@ -160,7 +160,8 @@ struct Slot {
 // (HEADS: heads first; else the heads of a token are D apart, which makes every
 // row's address a constant offset.)
 template <int D, bool INTER, bool HEADS, int U>
-__global__ void __launch_bounds__(kThreads, 4) fa_norm_rope_kernel(const __grid_constant__ NormRope p) {
+__global__ void __launch_bounds__(kThreads, 4)
+    fa_norm_rope_kernel(const __grid_constant__ NormRope p) {
     constexpr int LPR = D / 8, SL = kThreads / LPR;
     const Lane<D, INTER> lane(p.t.half);
     const bool is_q = static_cast<int>(blockIdx.x) < p.q.ctas;

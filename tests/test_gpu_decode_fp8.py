@@ -54,7 +54,8 @@ class Cache:
 
     def call(self, more=0, **kw):
         """`more`: entries of the table that no sequence has a use for; a few pages
-        a row take another way through the kernels than many."""
+        a row take another way through the kernels than many, and very many yet
+        another where more than 16 query heads share a K/V head."""
         table = self.table
         if more:
             shape = (more,) if table.dim() == 1 else (len(table), more)
@@ -66,7 +67,7 @@ class Cache:
         return o, lse
 
     def both(self):
-        for more in (0, 9):
+        for more in (0, 9, 1300):
             o, lse = self.call(more)
             _ok()
             self.check(o, lse)
