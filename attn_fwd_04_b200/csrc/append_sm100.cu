@@ -288,8 +288,9 @@ __global__ void __launch_bounds__(kThreads, 3)
 // A CTA takes one (sequence, block) of K or of V and some of its heads, one
 // after the other.  Each thread keeps its rows' values in registers between
 // the maximum and the rounding (4 rows: 64 tokens of 128 values a CTA; larger
-// blocks are read twice), and its positions' rotations for all heads; the next
-// heads' rows are on their way into shared memory meanwhile.
+// blocks are read twice); the next heads' rows are on their way into shared memory
+// meanwhile.  The positions' rotations are read from L1 again for each head (kept in
+// registers, 32 of them, blocks of 128 took 105 us instead of 93).
 //
 // 8 x 1024 tokens of 32 + 2 * 32 heads, blocks of 64: 80 us, 4.2 TB/s, 0.65 of a
 // copy; of it the queries 23 us (at their floor) and keys and values 57 (floor 31).
@@ -514,7 +515,7 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
     const bool norms = is_k && p.wk.w;
     Vec8 w = {};
     if (norms) w = lane.weights(p.wk);
-    Rotation<D, INTER> rot[UH];
+    int pos[UH];  // of the thread's tokens
     // Where the thread's tokens of chunk c lie, and which of them there are: rows
     // behind the last are that one again, and are not stored.
     const int64_t sx = is_k ? p.sk : p.sv;
@@ -531,8 +532,7 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
 #pragma unroll
         for (int i = 0; i < UH; ++i) {
             if (c * CH + i * SL + tok < rows) there |= 1u << i;
-            if (is_k)
-                rot[i].load(p.t, min(b.first + c * CH + i * SL + tok, b.last - 1), lane);
+            pos[i] = min(b.first + c * CH + i * SL + tok, b.last - 1);
         }
     };
     // A ring of chunks on their way: a slot's rows are copied, and read, by its
@@ -571,7 +571,11 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
         }
         if (is_k && lane.turns) {
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) rot[u % UH].turn(v[u]);
+            for (int u = 0; u < kRows; ++u) {
+                Rotation<D, INTER> rot;
+                rot.load(p.t, pos[u % UH], lane);
+                rot.turn(v[u]);
+            }
         }
     };
     const uint4* const slot_in_ring = ring + my * LPR;
