@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 // meanwhile.  The positions' rotations are read from L1 again for each head (kept in
 // registers, 32 of them, blocks of 128 took 105 us instead of 93).
 //
-// 8 x 1024 tokens of 32 + 2 * 32 heads, blocks of 64: 80 us, 4.2 TB/s, 0.65 of a
-// copy; of it the queries 23 us (at their floor) and keys and values 57 (floor 31).
+// 8 x 1024 tokens of 32 + 2 * 32 heads, blocks of 64: 79 us, 4.3 TB/s, 0.66 of a
+// copy; of it the queries 23 us (at their floor) and keys and values some 56 (31).
 // Those are bound by latency: a barrier a head, two CTAs of 128 registers an SM
 // (three spill: 109 us without the queries), the scheduler 46 % busy.  With the
 // rows read twice instead of kept, 132 us; with them fetched into registers one
@@ -688,7 +688,7 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
 // slot takes one head of K or of V (pairs pair_begin .. pair_end - 1, the keys
 // first), R tokens at a time, and finds its scale alone; where scales grow,
 // the CTA rounds the earlier tokens of those heads together.  A step of 64 tokens
-// with 32 + 2 * 8 heads takes 4.9 us, as into bf16 pages.
+// with 32 + 2 * 8 heads takes 4.5 us, as into bf16 pages.
 template <int D, bool INTER, int R>
 __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block b, int pair_begin,
                                            int pair_end) {
@@ -816,17 +816,19 @@ __device__ __forceinline__ bool find_block(const Append& p, int unit, Shared& sh
     return true;
 }
 
-// The first CTAs take units, unit_ctas of them: for each unit as many as
-// cover the heads of K and then those of V, unit_heads each (FEW: the heads of
-// both together).  The others take the queries' rows.
+// unit_ctas CTAs take units: for each unit as many as cover the heads of K and then
+// those of V, unit_heads each (FEW: the heads of both together).  The others take
+// the queries' rows: after them, as the lighter work, or (FEW, where all run at
+// once) before them, as the longer one.
 template <int D, bool INTER, bool FEW>
 __global__ void __launch_bounds__(kThreads, 2)
     fa_append_fp8_kernel(const __grid_constant__ Append p) {
     __shared__ Shared sh;
     extern __shared__ uint4 ring[];
-    const int cta = blockIdx.x;
-    if (cta >= p.unit_ctas) {
-        append_rows<D, INTER, false>(p, cta - p.unit_ctas, sh);
+    const int block = blockIdx.x, row_ctas = gridDim.x - p.unit_ctas;
+    const int cta = FEW ? block - row_ctas : block;
+    if (FEW ? cta < 0 : cta >= p.unit_ctas) {
+        append_rows<D, INTER, false>(p, FEW ? block : cta - p.unit_ctas, sh);
         return;
     }
     const int hgroups = (p.Hk + p.unit_heads - 1) / p.unit_heads;
@@ -848,20 +850,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int first = (is_k ? sub : sub - hgroups) * p.unit_heads;
         const int end = min(first + p.unit_heads, p.Hk);
         constexpr int SL = kThreads / (D / 8);
-        const int block = 1 << p.block_log2;
+        const int width = 1 << p.block_log2;
         auto run = [&](auto uh, auto parts, auto many) {
             append_block<D, INTER, decltype(uh)::value, decltype(parts)::value,
                          decltype(many)::value>(p, b, is_k, first, end, ring);
         };
         using std::integral_constant;
-        if (D == 64 && block < SL)
+        if (D == 64 && width < SL)
             run(integral_constant<int, 1>{}, integral_constant<int, D == 64 ? 2 : 1>{},
                 std::false_type{});
-        else if (block == SL)
+        else if (width == SL)
             run(integral_constant<int, 1>{}, integral_constant<int, 1>{}, std::false_type{});
-        else if (block == 2 * SL)
+        else if (width == 2 * SL)
             run(integral_constant<int, 2>{}, integral_constant<int, 1>{}, std::false_type{});
-        else if (block == 4 * SL)
+        else if (width == 4 * SL)
             run(integral_constant<int, 4>{}, integral_constant<int, 1>{}, std::false_type{});
         else
             run(integral_constant<int, 4>{}, integral_constant<int, 1>{}, std::true_type{});
