@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtas)
             if (norms) {
                 // with g' = g r:  dw += g' x,  dx = g' w - x r^2 mean(g' w x)
                 const Vec8 xv = lane.unpack(xr[u]);
-                const float r = row_rstd<D>(xv, p.eps);
+                float r = row_rstd<D>(xv, p.eps);
+                if (u >= count || bad) r = 0.f;  // (of zeros it is infinite where eps is 0)
                 gv = scale8(gv, r);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {

@@ -197,6 +197,32 @@ def test_positions_out_of_range_are_reported():
     assert (out[2] - part[2]).abs().max().item() <= 1e-4
 
 
+def test_no_epsilon():
+    """eps = 0: rows that a thread's group of heads lacks, and tokens out of range,
+    are no zeros to be normed."""
+    for layout in ("packed", "heads"):
+        q, k, pos, at = _inputs(layout, 7, 3, 1, 128, seed=9)
+        c, s = fa.fa_rope_table(700, 128)
+        w = torch.linspace(0.5, 1.5, 128, device="cuda")
+        g, gk = torch.randn_like(q), torch.randn_like(k)
+        yq, yk = fa.fa_qk_norm_rope(q, k, w, w, c, s, pos, eps=0.0)
+        out = fa.fa_qk_norm_rope_bwd(q, k, g, gk, w, w, c, s, pos, eps=0.0)
+        _ok()
+        for x, y, gx, dx, dw in ((q, yq, g, out[0], out[2]), (k, yk, gk, out[1], out[3])):
+            cr, sr = c[at.long()], s[at.long()]
+            _close(y, ref.norm_rope(_packed(x), w, cr, sr, False, 0.0))
+            rx, rw, size, sums = ref.norm_rope_bwd(_packed(x), _packed(gx), w, cr, sr, False, 0.0)
+            tol = 2.0 ** -8 * rx.abs() + 2.0 ** -18 * size.amax(-1, keepdim=True)
+            assert ((_packed(dx).double() - rx).abs() <= tol).all()
+            assert ((dw.double() - rw).abs() <= 2.0 ** -15 * sums).all()
+    q, k, pos, at = _inputs("packed", 7, 3, 1, 128, seed=9)
+    pos = pos.clone()
+    pos[3] = 700
+    out = fa.fa_qk_norm_rope_bwd(q, k, q, k, w, w, c, s, pos, eps=0.0)
+    assert fa.fa_get_device_error() == fa.FA_ERR_DEVICE_BAD_INPUT
+    assert all(torch.isfinite(t).all() for t in out) and (out[0][3] == 0).all()
+
+
 def test_no_tokens():
     q, k = torch.empty((0, 4, 128)).bfloat16().cuda(), torch.empty((0, 2, 128)).bfloat16().cuda()
     w = torch.ones(128, device="cuda")
