@@ -63,9 +63,9 @@ class Case:
         self.pos = torch.cat([torch.arange(c, c + n) for n, c in zip(new, ctx)]).long().cuda() \
             if total else torch.zeros(0, dtype=torch.long, device="cuda")
 
-    def call(self, with_q=True, **kw):
+    def call(self, with_q=True, eps=1e-5, **kw):
         args = dict(rope_cos=self.cos, rope_sin=self.sin, q_weight=self.qw if with_q else None,
-                    k_weight=self.kw, eps=1e-5, **kw)
+                    k_weight=self.kw, eps=eps, **kw)
         q = self.q if with_q else None
         t = self.table.cuda()
         if self.block:
@@ -355,6 +355,21 @@ def test_a_rotation_and_append_equal_the_calls_one_by_one():
     fa.fa_append_paged(k2, c.v.contiguous(), c.cu, kp, vp, c.table.cuda(), c.seq)
     _ok()
     assert torch.equal(q, q2) and torch.equal(c.kp, kp) and torch.equal(c.vp, vp)
+
+
+@pytest.mark.parametrize("block", [0, 16, 64, 256])
+def test_no_epsilon(block):
+    """eps = 0 gives what an eps below half a step of any row's mean square gives: the
+    rows that a thread's group of tokens or heads lacks are not taken for zeros."""
+    for new, ctx in (([3, 1, 2], [60, 0, 255]), ([70, 5, 300], [3, 250, 0])):
+        got = []
+        for eps in (0.0, 1e-30):
+            c = Case(new, ctx, 7, 3, 128, 64, "fp32", "rows", block, seed=6)
+            got.append([c.call(eps=eps), c.kp.view(torch.uint8), c.vp.view(torch.uint8)] +
+                       ([c.ks, c.vs] if block else []))
+        _ok()
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+        assert torch.isfinite(got[0][0]).all()
 
 
 @pytest.mark.parametrize("block", [0, 64])
