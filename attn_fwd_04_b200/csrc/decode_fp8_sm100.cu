@@ -42,10 +42,12 @@
 // take 4.
 //
 // Rounding: each query row is scaled by a power of two into fp16, which holds
-// its 8 bits exactly; scores, maxima and sums are fp32; weights p * vscale are
-// rounded to fp16 (11 bits), scaled by a power of two that follows the largest
-// value scale so far, so that block scales may differ by 2^28 before small
-// ones lose bits.
+// its 8 bits exactly down to 2^-31 of the row's largest; scores, maxima and sums
+// are fp32.  Weights p * vscale are held relative to the largest of them so far, for
+// each query head: the running maximum m is that of the scores with log2 vscale
+// added, so that a block of large values that the softmax hardly sees does not
+// push the others out of fp16's range, whatever the scales.  They are rounded to
+// fp16: 11 bits, or 2^-40 of the largest.
 #include <algorithm>
 #include <cmath>
 
@@ -236,6 +238,19 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// 2^x down to the least subnormal: where a weight below 2^-126 may meet a value that
+// is larger than the others' by more than that.
+__device__ __forceinline__ float ex2_gradual(float x) {
+    const float y = ex2_approx(0.5f * x);
+    return y * y;
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Cache bytes are read once: kept out of L1, and in the order written here.
@@ -478,8 +493,11 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         const uint8_t* base = p.kp + x.slice * (kPage * D) + 16 * t;
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-            ks[m] = __ldg(p.ks + (x.slice << nb_log2) +
-                          (min(slot0 + 16 * m, last) >> p.block_log2));
+            // (both scales: the softmax wants V's with the scores)
+            const int64_t scale =
+                (x.slice << nb_log2) + (min(slot0 + 16 * m, last) >> p.block_log2);
+            ks[m] = __ldg(p.ks + scale);
+            vs[m] = __ldg(p.vs + scale);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 // behind the last token: that token again
@@ -493,14 +511,11 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         const int slot0 = (x.tile * TILE) % kPage, last = slot0 + x.len - 1 - x.tile * TILE;
         const uint8_t* base = p.vp + x.slice * (kPage * D) + D / 8 * g;
 #pragma unroll
-        for (int m = 0; m < M; ++m) {
-            vs[m] = __ldg(p.vs + (x.slice << nb_log2) +
-                          (min(slot0 + 16 * m, last) >> p.block_log2));
+        for (int m = 0; m < M; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 load_bytes(vr[RING ? 0 : m][i],
                            base + min(slot0 + 16 * m + 2 * t + (i & 1) + 8 * (i >> 1), last) * D);
-        }
     };
 
     // the same by way of the ring: tiles asked for, and taken, in turn
@@ -570,7 +585,6 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
     };
 
     float o[NT][MT][4], m_run[NT][2], l_run[NT][2], fac[NT][2];
-    float v_top = 0.f;  // power of two, at least every value scale so far
     // A new head of a sequence: its queries as fragments, and an empty state.
     auto begin = [&](int b, int hk) {
 #pragma unroll
@@ -622,7 +636,6 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.f;
         }
-        v_top = 0x1p-64f;
     };
 
     if constexpr (RING) {
@@ -681,23 +694,16 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 }
             }
         }
-        float k_scale[M], v_weight[M];
-        uint32_t v_most = 0;
+        float k_scale[M], v_weight[M], v_log[M];
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             k_scale[m] = ks[m];
-            v_weight[m] = vs[m];
-            v_most = max(v_most, __float_as_uint(vs[m]));
+            v_weight[m] = vs[m] * 0x1p15f;
+            v_log[m] = fmaxf(lg2_approx(vs[m]), -64.f);
         }
         if (!RING && more) load_k(c);
         // ---- softmax over the tile's tokens ---------------------------------------
-        const float v_new = fmaxf(
-            v_top, __uint_as_float((v_most + 0x7fffffu) & 0x7f800000u));
-        // 2^15 / v_new
-        const float up = __uint_as_float((269u << 23) - __float_as_uint(v_new));
-#pragma unroll
-        for (int m = 0; m < M; ++m) v_weight[m] *= up;
-        bool moved = v_new != v_top;
+        bool moved = false;
         float keep[NT][2];
         uint32_t pf[NT][M][2];
 #pragma unroll
@@ -711,15 +717,16 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float top = fmaxf(sc[nt][0][i], sc[nt][0][i + 2]);
+                float top = fmaxf(sc[nt][0][i], sc[nt][0][i + 2]) + v_log[0];
 #pragma unroll
-                for (int m = 1; m < M; ++m) top = max3f(top, sc[nt][m][i], sc[nt][m][i + 2]);
+                for (int m = 1; m < M; ++m)
+                    top = fmaxf(top, fmaxf(sc[nt][m][i], sc[nt][m][i + 2]) + v_log[m]);
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 const float m_new = fmaxf(m_run[nt][i], top);
                 const float base = m_new == -INFINITY ? 0.f : m_new;
-                keep[nt][i] = ex2_approx(m_run[nt][i] - base);
+                keep[nt][i] = ex2_gradual(m_run[nt][i] - base);
                 moved = moved || m_new != m_run[nt][i];
                 m_run[nt][i] = m_new;
                 float sum = 0.f;
@@ -741,19 +748,16 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                                                            sc[nt][m][2 * h + 1] * v_weight[m]));
         }
         if (__any_sync(0xffffffffu, moved)) {
-            const float down = v_top / v_new;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float k_0 = keep[nt][0] * down, k_1 = keep[nt][1] * down;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    o[nt][mt][0] *= k_0;
-                    o[nt][mt][1] *= k_1;
-                    o[nt][mt][2] *= k_0;
-                    o[nt][mt][3] *= k_1;
+                    o[nt][mt][0] *= keep[nt][0];
+                    o[nt][mt][1] *= keep[nt][1];
+                    o[nt][mt][2] *= keep[nt][0];
+                    o[nt][mt][3] *= keep[nt][1];
                 }
             }
-            v_top = v_new;
         }
         // ---- O^T += V^T P^T ----------------------------------------------------------
 #pragma unroll
@@ -789,7 +793,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 const int hh = nt * 8 + 2 * t + i;
                 if (hh >= heads) continue;
                 const float lse2 = m_run[nt][i] + log2f(l);
-                const float inv = (l == 0.f ? 0.f : 1.f / l) * (v_top * 0x1p-15f);
+                const float inv = l == 0.f ? 0.f : 0x1p-15f / l;
                 if (whole) {
                     const int64_t row =
                         static_cast<int64_t>(b) * p.H + hk * p.G + group * p.group_heads + hh;
@@ -830,7 +834,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 const int hh = nt * 8 + 2 * t + i;
-                const float inv = (l == 0.f ? 0.f : 1.f / l) * (v_top * 0x1p-15f);
+                const float inv = l == 0.f ? 0.f : 0x1p-15f / l;
                 if (g == 0) lse_sh[warp][hh] = m_run[nt][i] + log2f(l);
                 float* dst = &acc_sh[warp][hh][D / 8 * g];
 #pragma unroll
@@ -853,7 +857,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             const float base = top == -INFINITY ? 0.f : top;
             Joined j{make_float4(0.f, 0.f, 0.f, 0.f), 0.f};
             for (int w = 0; w < n; ++w) {
-                const float f = ex2_approx(lse_of(w) - base);
+                const float f = ex2_gradual(lse_of(w) - base);
                 const float4 x = value_of(w);
                 sum += f;
                 j.a.x = fmaf(f, x.x, j.a.x);
@@ -1004,14 +1008,14 @@ __global__ void __launch_bounds__(merge_warps(ROW) * 32)
         float m = top;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) m = fmaxf(m, lse[k]);
-        const float base = m == -INFINITY ? 0.f : m, keep = ex2_approx(top - base);
+        const float base = m == -INFINITY ? 0.f : m, keep = ex2_gradual(top - base);
         top = m;
         sum *= keep;
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] *= keep;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const float w = ex2_approx(lse[k] - base);
+            const float w = ex2_gradual(lse[k] - base);
             sum += w;
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[j] = fmaf(w, x[k][j], acc[j]);
@@ -1035,7 +1039,7 @@ __global__ void __launch_bounds__(merge_warps(ROW) * 32)
         for (int j = 0; j < V; ++j) acc[j] = 0.f;
 #pragma unroll
         for (int w = 0; w < ROW; ++w) {
-            const float f = ex2_approx(top_sh[w] - base);
+            const float f = ex2_gradual(top_sh[w] - base);
             sum = fmaf(f, sum_sh[w], sum);
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[j] = fmaf(f, acc_sh[w][V * lane + j], acc[j]);

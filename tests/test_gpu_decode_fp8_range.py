@@ -1,0 +1,94 @@
+"""Decode over the 8-bit cache where the blocks' scales lie far apart: what a block
+weighs in the output is its softmax weight times its value scale, and neither
+alone."""
+import math
+
+import pytest
+import torch
+
+import attn_fwd_04_b200 as fa
+import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+PS = 256
+FP8 = torch.float8_e4m3fn
+LOG2E = 1.4426950408889634
+
+
+def pool(lens, H, Hk, d, block, seed):
+    """Queries near one direction u of signs for each K/V head, codes of all kinds."""
+    g = torch.Generator().manual_seed(seed)
+    P = sum(ref.pages_of(lens))
+    u = torch.randint(0, 2, (Hk, d), generator=g) * 2.0 - 1
+    q = (u.repeat_interleave(H // Hk, 0) * (1 + 0.25 * torch.rand((len(lens), H, d), generator=g)))
+    kp, vp = ((torch.randn((P, Hk, PS, d), generator=g) * 100).clamp(-448, 448).to(FP8)
+              for _ in range(2))
+    ks = torch.full((P, Hk, PS // block), 0.002)
+    vs = 0.01 * torch.exp2(torch.rand((P, Hk, PS // block), generator=g) - 0.5)
+    table = torch.randperm(P, generator=g).int()
+    return u, q.bfloat16().cuda(), kp.cuda(), vp.cuda(), ks.cuda(), vs.cuda(), table
+
+
+def block_of(table, lens, b, pos, block):
+    """Page and block in it of position pos of sequence b."""
+    return ref.page_list(table, lens, b)[pos // PS], pos % PS // block
+
+
+def check(q, kp, vp, ks, vs, table, lens, bits=11):
+    scale = q.shape[2] ** -0.5
+    r, rl, absv, reach = ref.decode(q, kp, vp, ks, vs, table, lens, scale)
+    # the largest p * vscale of each head, by the same call on codes of one
+    ones = torch.ones_like(vp.float()).to(FP8)
+    total = ref.decode(q, kp, ones, ks, vs, table, lens, scale)[0].amax(-1)
+    n = torch.tensor(lens, device="cuda")[:, None]
+    delta = 2.0 ** -16 * reach
+    # (scores less a maximum of up to 64 and more lie 2^-17 apart in fp32)
+    weights = 2.0 ** -bits + 4 * delta + 2.0 ** -17 + 2.0 ** -22 * n
+    # and each weight within 2^-40 of the largest, which is at most their sum, times 448
+    tol = 2.0 ** -8 * r.abs() + weights[..., None] * absv + \
+        (2.0 ** -40 * 448 * n * total)[..., None]
+    # tables of several widths take the kernels' several ways
+    for more in (0, 9, 1300):
+        t = torch.cat([table, torch.full((more,), -1, dtype=torch.int32)]).cuda()
+        lse = torch.empty(q.shape[:2], device="cuda")
+        o = fa.fa_decode_paged_fp8(q, kp, vp, ks, vs, t, torch.tensor(lens).int().cuda(), lse=lse)
+        assert fa.fa_get_device_error() == fa.FA_OK
+        assert torch.isfinite(o).all()
+        over = ((o.double() - r).abs() - tol).max().item()
+        assert over <= 0, (more, over)
+        assert ((lse.double() - rl).abs() <= 2 * delta + 2.0 ** -17 * (1 + rl.abs()) +
+                2.0 ** -22 * n).all()
+    return r
+
+
+@pytest.mark.parametrize("H,Hk,d,block", [(4, 1, 128, 32), (8, 2, 64, 16), (16, 1, 128, 16),
+                                          (32, 1, 64, 64), (24, 1, 128, 64)])
+@pytest.mark.parametrize("ratio", [30, 44, 100, 127])
+@pytest.mark.parametrize("at", ["first", "last"])
+def test_a_large_block_that_the_softmax_hardly_sees(H, Hk, d, block, ratio, at):
+    """One block's value scale 2^ratio times the others', its tokens' weights 2^-ratio
+    of theirs (the first sequence: it gives about as much as they do) or less."""
+    lens = [700, 5000, 300]
+    u, q, kp, vp, ks, vs, table = pool(lens, H, Hk, d, block, seed=ratio)
+    vs *= 100 * 2.0 ** -(ratio / 2)
+    for b, n in enumerate(lens):
+        pos = 0 if at == "first" else (n - 1) // block * block
+        p, i = block_of(table, lens, b, pos, block)
+        rows = slice(i * block, (i + 1) * block)
+        kp[p, :, rows] = (-256.0 * u).to(FP8).cuda()[:, None]
+        # (a query's product with it is about 288 d)
+        ks[p, :, i] = ratio * (1 + b / 2) / LOG2E / (288 * d ** 0.5)
+        vs[p, :, i] = 2.0 ** (ratio / 2)
+    check(q, kp, vp, ks, vs, table, lens)
+
+
+def test_zero_codes_under_a_larger_scale():
+    """The small blocks' values come through beside a large block of zeros."""
+    lens = [600, 40]
+    for shift in (4, 12, 20):
+        u, q, kp, vp, ks, vs, table = pool(lens, 4, 1, 128, 16, seed=shift)
+        for b in range(2):
+            p, i = block_of(table, lens, b, 16, 16)
+            vp[p, 0, 16 * i:16 * i + 16] = 0.0
+            vs[p, 0, i] = 0.01 * 2.0 ** shift
+        check(q, kp, vp, ks, vs, table, lens)
