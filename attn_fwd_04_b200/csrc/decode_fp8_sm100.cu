@@ -46,8 +46,10 @@
 // are fp32.  Weights p * vscale are held relative to the largest of them so far, for
 // each query head: the running maximum m is that of the scores with log2 vscale
 // added, so that a block of large values that the softmax hardly sees does not
-// push the others out of fp16's range, whatever the scales.  They are rounded to
-// fp16: 11 bits, or 2^-40 of the largest.
+// push the others out of fp16's range, whatever the scales.  A weight is the sum of
+// two fp16 values (22 bits, or 2^-40 of the largest), each with a product of its own:
+// with one alone an output differed by 1e-3 of its size from that of fp32 weights, now
+// by 2e-4 and less, which is what bf16 makes of fp32 sums in another order.
 #include <algorithm>
 #include <cmath>
 
@@ -238,6 +240,17 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// (lo, hi) as the sum of two fp16 pairs.
+__device__ __forceinline__ void split_f16x2(float lo, float hi, uint32_t& a, uint32_t& b) {
+    a = pack_f16x2(lo, hi);
+    float back_lo, back_hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(back_lo), "=f"(back_hi)
+        : "r"(a));
+    b = pack_f16x2(lo - back_lo, hi - back_hi);
 }
 
 // 2^x down to the least subnormal: where a weight below 2^-126 may meet a value that
@@ -705,7 +718,7 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
         // ---- softmax over the tile's tokens ---------------------------------------
         bool moved = false;
         float keep[NT][2];
-        uint32_t pf[NT][M][2];
+        uint32_t pf[NT][M][2], pr[NT][M][2];  // weights, and what fp16 leaves of them
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -743,9 +756,13 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    pf[nt][m][h] = transpose8x8(pack_f16x2(sc[nt][m][2 * h] * v_weight[m],
-                                                           sc[nt][m][2 * h + 1] * v_weight[m]));
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t a, b;
+                    split_f16x2(sc[nt][m][2 * h] * v_weight[m],
+                                sc[nt][m][2 * h + 1] * v_weight[m], a, b);
+                    pf[nt][m][h] = transpose8x8(a);
+                    pr[nt][m][h] = transpose8x8(b);
+                }
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
@@ -772,8 +789,10 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
                     cvt4(__byte_perm(vr[from][0][w], vr[from][1][w], hi ? 0x7362 : 0x5140), a0, a1);
                     cvt4(__byte_perm(vr[from][2][w], vr[from][3][w], hi ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
                         mma_f16(o[nt][2 * w + hi], a0, a1, a2, a3, pf[nt][m][0], pf[nt][m][1]);
+                        mma_f16(o[nt][2 * w + hi], a0, a1, a2, a3, pr[nt][m][0], pr[nt][m][1]);
+                    }
                 }
             }
         }

@@ -611,10 +611,9 @@ FA_API int fa_append_paged_fp8(const void* q_new, const void* k_new, const void*
  *              treated as 0 and reported as FA_ERR_DEVICE_BAD_INPUT
  *   lse      : NULL, or fp32 [B, H]: natural log of the sum of exponentials
  *   scale    : softmax scale (normally 1/sqrt(d))
- * Scores, maxima and sums are fp32.  The weights p * v_scale are held to 11 bits,
+ * Scores, maxima and sums are fp32.  The weights p * v_scale are held to 22 bits,
  * or to 2^-40 of the largest of a sequence's and query head's where that is more
- * (so a block of zero codes hides others only by a scale 2^28 times theirs and
- * weights as large).
+ * (beside a weight 2^28 times theirs, of zero codes say, others keep 12 bits).
  * H is any multiple of H_kv; query head h reads K/V head h / (H / H_kv).  A
  * sequence longer than its table's entries is reported and cut to them; a page
  * index outside [0, num_pages) is reported and that sequence's output is

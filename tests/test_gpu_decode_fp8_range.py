@@ -92,3 +92,24 @@ def test_zero_codes_under_a_larger_scale():
             vp[p, 0, 16 * i:16 * i + 16] = 0.0
             vs[p, 0, i] = 0.01 * 2.0 ** shift
         check(q, kp, vp, ks, vs, table, lens)
+
+
+@pytest.mark.parametrize("G", [1, 4, 8, 16, 24, 32])
+@pytest.mark.parametrize("d,block", [(128, 16), (64, 64)])
+def test_weights_of_22_bits(G, d, block):
+    """Zero queries: each weight is its value scale, of 24 random bits.  Two fp16 values
+    hold it to 2^-22; the exponential, the division and the sums in fp32 add 2^-22 each,
+    the sums once a token.  An output is one of the two bf16 values that the ends of
+    that interval round to."""
+    lens = [1, 1, 1, 16, 100, 0, 33]
+    u, q, kp, vp, ks, vs, table = pool(lens, 2 * G, 2, d, block, seed=G)
+    q.zero_()
+    r, _, absv, _ = ref.decode(q, kp, vp, ks, vs, table, lens, 1.0)
+    n = torch.tensor(lens, device="cuda")[:, None, None]
+    off = (2.0 ** -20 + 2.0 ** -22 * n) * absv
+    low, high = (r - off).bfloat16(), (r + off).bfloat16()
+    for more in (0, 9, 1300):
+        t = torch.cat([table, torch.full((more,), -1, dtype=torch.int32)]).cuda()
+        o = fa.fa_decode_paged_fp8(q, kp, vp, ks, vs, t, torch.tensor(lens).int().cuda())
+        assert fa.fa_get_device_error() == fa.FA_OK
+        assert ((low <= o) & (o <= high)).all()
