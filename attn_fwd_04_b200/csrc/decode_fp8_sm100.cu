@@ -725,7 +725,8 @@ __global__ void __launch_bounds__((SOLO ? SOLO : kWarps) * 32,
             for (int m = 0; m < M; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    sc[nt][m][i] = sc[nt][m][i] * fac[nt][i & 1] * k_scale[m];
+                    // (in this order neither product leaves fp32 where the score does not)
+                    sc[nt][m][i] = sc[nt][m][i] * k_scale[m] * fac[nt][i & 1];
                     if (tok0 + 16 * m + 8 * (i >> 1) + g >= len) sc[nt][m][i] = -INFINITY;
                 }
 #pragma unroll

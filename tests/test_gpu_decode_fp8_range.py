@@ -113,3 +113,22 @@ def test_weights_of_22_bits(G, d, block):
         o = fa.fa_decode_paged_fp8(q, kp, vp, ks, vs, t, torch.tensor(lens).int().cuda())
         assert fa.fa_get_device_error() == fa.FA_OK
         assert ((low <= o) & (o <= high)).all()
+
+
+@pytest.mark.parametrize("G", [1, 16])
+def test_large_queries_over_small_keys(G):
+    """Queries of 2^126 and keys under a scale of 2^-64: the scores, up to 2^80, are in
+    fp32's range, and the largest takes all of the weight."""
+    lens = [1, 40]
+    u, q, kp, vp, ks, vs, table = pool(lens, G, 1, 64, 64, seed=1)
+    q = (u.repeat(2, G, 1) * 2.0 ** 126).bfloat16().cuda()
+    ks.fill_(2.0 ** -64)
+    p = ref.page_list(table, lens, 1)[0]
+    kp[p, 0, 17] = (448.0 * u[0]).to(FP8).cuda()
+    o = fa.fa_decode_paged_fp8(q, kp, vp, ks, vs, table.cuda(), torch.tensor(lens).int().cuda(),
+                               scale=1.0)
+    assert fa.fa_get_device_error() == fa.FA_OK
+    for b, at in ((0, 0), (1, 17)):
+        p = ref.page_list(table, lens, b)[0]
+        want = vp[p, 0, at].double() * vs[p, 0, 0].double()
+        assert ((o[b].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -18) * want.abs()).all()
