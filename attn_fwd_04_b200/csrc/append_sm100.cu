@@ -532,7 +532,7 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
 #pragma unroll
         for (int i = 0; i < UH; ++i) {
             if (c * CH + i * SL + tok < rows) there |= 1u << i;
-            pos[i] = min(b.first + c * CH + i * SL + tok, b.last - 1);
+            pos[i] = b.first + min(c * CH + i * SL + tok, rows - 1);
         }
     };
     // A ring of chunks on their way: a slot's rows are copied, and read, by its
@@ -810,7 +810,7 @@ __device__ __forceinline__ bool find_block(const Append& p, int unit, Shared& sh
     const int start = s.len - s.n;
     b.lo = blk << p.block_log2;
     b.first = max(b.lo, start);
-    b.last = min(b.lo + (1 << p.block_log2), s.len);
+    b.last = b.lo + min(1 << p.block_log2, s.len - b.lo);  // (lo + a block may pass 2^31)
     b.row = s.row0 + (b.first - start);
     b.at = b.lo % kPage;
     return true;
