@@ -132,3 +132,28 @@ def test_large_queries_over_small_keys(G):
         p = ref.page_list(table, lens, b)[0]
         want = vp[p, 0, at].double() * vs[p, 0, 0].double()
         assert ((o[b].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -18) * want.abs()).all()
+
+
+@pytest.mark.parametrize("H,d", [(1, 64), (16, 64), (4, 128)])
+def test_a_sequence_of_2_31_tokens(H, d):
+    """2^31 - 1 tokens (a packed table may name one page many times): the last tile
+    ends where the sequence does.  The last token, on a page of its own, has weight
+    e^34 beside the others' 1, and the slot behind it holds it once more."""
+    lens = [2 ** 31 - 1]
+    kp, vp = (torch.zeros((2, 1, PS, d), device="cuda").to(FP8) for _ in range(2))
+    kp[1, 0, 254:] = torch.tensor(16.0).to(FP8)
+    vp[:] = torch.tensor(2.0).to(FP8)
+    vp[1, 0, 254:] = torch.tensor(-3.0).to(FP8)
+    ks, vs = (torch.ones((2, 1, 1), device="cuda") for _ in range(2))
+    table = torch.zeros(2 ** 23, dtype=torch.int32, device="cuda")
+    table[-1] = 1
+    q = torch.ones((1, H, d), device="cuda").bfloat16()
+    lse = torch.empty((1, H), device="cuda")
+    scale = 34.0 / (16 * d)
+    o = fa.fa_decode_paged_fp8(q, kp, vp, ks, vs, table, torch.tensor(lens).int().cuda(),
+                               scale=scale, lse=lse)
+    assert fa.fa_get_device_error() == fa.FA_OK
+    # 2^31 - 2 weights of 1 and one of e^34 = 5.8e14: 3.7e-6 of the sum
+    want = math.log(math.exp(34.0) + 2.0 ** 31 - 2)
+    assert (lse.double() - want).abs().max().item() <= 2.0 ** -18 * 35 + 2.0 ** -16 * 34
+    assert ((o.double() + 3).abs() <= 3 * 2.0 ** -8 + 2.0 ** -16).all()
