@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libfa.so")
 CALLS = os.path.join(PKG, "_calls.so")
 SOURCES = ["api.cu", "fwd_sm100.cu", "bwd_sm100.cu", "decode_sm100.cu", "decode_noalloc.cu",
            "rope_sm100.cu", "append_sm100.cu", "decode_fp8_sm100.cu"]
-HEADERS = ["fa_ptx.cuh", "fa_internal.h", "rope_row.cuh"]
+HEADERS = ["fa_ptx.cuh", "fa_internal.h", "rope_row.cuh", "workspace.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -6,7 +6,6 @@
 #include <cstring>
 #include <atomic>
 #include <mutex>
-#include <vector>
 
 #include "fa_ptx.cuh"
 
@@ -30,20 +29,14 @@ __device__ unsigned int g_device_error = 0;
 
 constexpr int kMaxDevices = 64;
 
-// One grow-only workspace per stream (decode partials, rotated K, backward
-// scratch, page offsets): calls on different streams never share scratch.
-struct StreamWorkspace {
-    cudaStream_t stream = nullptr;
-    void* ptr = nullptr;
-    size_t bytes = 0;
-};
-
 struct DeviceState {
     bool init = false;
     int num_sms = 0;
     int cc_major = 0;
     unsigned int* err = nullptr;  // device address of g_device_error
-    std::vector<StreamWorkspace> ws;
+    // One grow-only workspace per stream (decode partials, rotated K, backward
+    // scratch, page offsets): calls on different streams never share scratch.
+    fa::StreamBlocks ws;
 };
 
 std::mutex g_mu;
@@ -128,16 +121,16 @@ int make_map_f32(CUtensorMap* map, const void* base, const cuuint64_t dims[3],
 }
 
 // The stream's grow-only workspace on this device, allocated (and, when it
-// grows, freed) in the stream's own order.
-int ensure_workspace(DeviceState* s, size_t bytes, cudaStream_t stream, void** out) {
-    std::lock_guard<std::mutex> lock(g_mu);
-    StreamWorkspace* w = nullptr;
-    for (StreamWorkspace& e : s->ws)
-        if (e.stream == stream) w = &e;
-    if (!w) {
-        s->ws.push_back(StreamWorkspace{stream, nullptr, 0});
-        w = &s->ws.back();
+// grows, freed) in the stream's own order; the caller keeps `hold` until its
+// last launch.
+int ensure_workspace(DeviceState* s, size_t bytes, cudaStream_t stream, void** out,
+                     fa::WorkspaceHold* hold) {
+    try {
+        *hold = s->ws.take(stream);
+    } catch (...) {
+        return FA_ERR_NOMEM;
     }
+    fa::WorkspaceHold& w = *hold;
     if (w->bytes < bytes) {
         if (w->ptr) {
             if (cudaFreeAsync(w->ptr, stream) != cudaSuccess) return FA_ERR_CUDA;
@@ -162,11 +155,12 @@ int ensure_workspace(DeviceState* s, size_t bytes, cudaStream_t stream, void** o
 // sequences' cached lengths differ widely: 1.8 % faster on the paged-prefill
 // workload); the variable-length forward pass measured no gain from it.
 int order_sequences(DeviceState* s, const int32_t* cu_seqlens, const int32_t* ctx_lens, int B,
-                    int causal, cudaStream_t stream, const int32_t** order) {
+                    int causal, cudaStream_t stream, const int32_t** order,
+                    fa::WorkspaceHold* hold) {
     *order = nullptr;
     if (B < 2 || B > fa::kSeqOrderMax) return FA_OK;
     void* ws = nullptr;
-    int rc = ensure_workspace(s, sizeof(int32_t) * static_cast<size_t>(B), stream, &ws);
+    int rc = ensure_workspace(s, sizeof(int32_t) * static_cast<size_t>(B), stream, &ws, hold);
     if (rc != FA_OK) return rc;
     int32_t* o = static_cast<int32_t*>(ws);
     if ((rc = fa::launch_seq_order(cu_seqlens, ctx_lens, B, causal ? 1 : 0, o, stream)) != FA_OK)
@@ -187,7 +181,8 @@ int device_error_word(unsigned int** err, int* num_sms) {
     return FA_OK;
 }
 
-int call_workspace(void* workspace, int given, size_t need, cudaStream_t stream, void** out) {
+int call_workspace(void* workspace, int given, size_t need, cudaStream_t stream, void** out,
+                   WorkspaceHold* hold) {
     if (workspace) {
         if (given < 0 || static_cast<size_t>(given) < need) return FA_ERR_SHAPE;
         *out = workspace;
@@ -199,7 +194,7 @@ int call_workspace(void* workspace, int given, size_t need, cudaStream_t stream,
     DeviceState* s = nullptr;
     int rc = lookup_device(&s);
     if (rc != FA_OK) return rc;
-    return ensure_workspace(s, need, stream, out);
+    return ensure_workspace(s, need, stream, out, hold);
 }
 }  // namespace fa
 
@@ -228,6 +223,7 @@ int fwd_fixed(const void* q, const void* k, const void* v, void* o, float* lse, 
     int rc = lookup_device(&s);
     if (rc != FA_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    fa::WorkspaceHold hold;
     const void* k_use = k;
     const void* q_use = q;
     if (rope_cos) {
@@ -236,7 +232,7 @@ int fwd_fixed(const void* q, const void* k, const void* v, void* o, float* lse, 
         void* ws = nullptr;
         const size_t kbytes = static_cast<size_t>(B) * H_kv * N * d * 2;
         const size_t qbytes = static_cast<size_t>(B) * H * N * d * 2;
-        if ((rc = ensure_workspace(s, kbytes + qbytes, st, &ws)) != FA_OK) return rc;
+        if ((rc = ensure_workspace(s, kbytes + qbytes, st, &ws, &hold)) != FA_OK) return rc;
         void* kr = ws;
         void* qr = static_cast<uint8_t*>(ws) + kbytes;
         if ((rc = fa::launch_rope_rows(k, kr, static_cast<int64_t>(B) * H_kv, q, qr,
@@ -328,7 +324,8 @@ int fa_bwd_gqa(const void* q, const void* k, const void* v, const void* o, const
     if ((rc = make_map(&tdo, dout, dims, strides, box)) != FA_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if ((rc = ensure_workspace(s, fa::bwd_workspace_bytes(B, H, N, d), st, &ws)) != FA_OK)
+    fa::WorkspaceHold hold;
+    if ((rc = ensure_workspace(s, fa::bwd_workspace_bytes(B, H, N, d), st, &ws, &hold)) != FA_OK)
         return rc;
     // the fp32 dQ accumulator [B*H, N, d] in the workspace, reduced into by TMA
     CUtensorMap tdq;
@@ -387,7 +384,9 @@ int fa_bwd_varlen(const void* q, const void* k, const void* v, const void* o, co
     if ((rc = make_map(&tdo, dout, dims, strides, box)) != FA_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if ((rc = ensure_workspace(s, fa::bwd_workspace_bytes(1, H, total, d), st, &ws)) != FA_OK)
+    fa::WorkspaceHold hold;
+    if ((rc = ensure_workspace(s, fa::bwd_workspace_bytes(1, H, total, d), st, &ws, &hold)) !=
+        FA_OK)
         return rc;
     // the fp32 dQ accumulator, head-major [H, total, d] in the workspace (a
     // tile's rows contiguous), reduced into by TMA
@@ -508,7 +507,8 @@ int fa_prefill_paged(const void* q, const void* k_pages, const void* v_pages,
     p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     p.err = s->err;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if ((rc = order_sequences(s, cu_q, seq_lens, B, causal, st, &p.seq_order)) != FA_OK)
+    fa::WorkspaceHold hold;
+    if ((rc = order_sequences(s, cu_q, seq_lens, B, causal, st, &p.seq_order, &hold)) != FA_OK)
         return rc;
     return fa::launch_fwd(p, tq, tk, tv, d, fa::kPaged, st);
 }
@@ -559,7 +559,8 @@ int decode_impl(const void* q, const void* k_pages, const void* v_pages,
     const size_t pack_bytes =
         max_pages > 0 ? (static_cast<size_t>(B) * max_pages + B) * sizeof(int32_t) : 0;
     void* ws = nullptr;
-    if ((rc = ensure_workspace(s, dec_bytes + pack_bytes, st, &ws)) != FA_OK) return rc;
+    fa::WorkspaceHold hold;
+    if ((rc = ensure_workspace(s, dec_bytes + pack_bytes, st, &ws, &hold)) != FA_OK) return rc;
     const int32_t* table = page_table;
     const int32_t* lens = seq_lens;
     if (max_pages > 0) {
@@ -616,7 +617,8 @@ int fa_gather_paged(const void* pages, const int32_t* page_table, const int32_t*
     if (rc != FA_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if ((rc = ensure_workspace(s, fa::decode_workspace_bytes(B, H, d, 1), st, &ws)) != FA_OK)
+    fa::WorkspaceHold hold;
+    if ((rc = ensure_workspace(s, fa::decode_workspace_bytes(B, H, d, 1), st, &ws, &hold)) != FA_OK)
         return rc;
     return fa::launch_gather(pages, page_table, seq_lens, out, B, H, d, page_size, ws, s->err,
                              s->num_sms, st);
@@ -639,7 +641,9 @@ int fa_append_paged(const void* k_new, const void* v_new, const int32_t* cu_new,
     if (total_new == 0) return FA_OK;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* ws = nullptr;
-    if ((rc = ensure_workspace(s, fa::decode_workspace_bytes(B, H_kv, d, 1), st, &ws)) != FA_OK)
+    fa::WorkspaceHold hold;
+    if ((rc = ensure_workspace(s, fa::decode_workspace_bytes(B, H_kv, d, 1), st, &ws, &hold)) !=
+        FA_OK)
         return rc;
     return fa::launch_append(k_new, v_new, cu_new, k_pages, v_pages, page_table, seq_lens, B,
                              H_kv, total_new, d, page_size, num_pages, ws, s->err, s->num_sms,
@@ -706,8 +710,9 @@ int fa_selftest_decode_stall(const void* q, const void* k_pages, const void* v_p
     if (rc != FA_OK) return rc;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     void* ws = nullptr;
+    fa::WorkspaceHold hold;
     if ((rc = ensure_workspace(s, fa::decode_workspace_bytes(B, H, d, fa::kDecodeMaxSplits), st,
-                               &ws)) != FA_OK)
+                               &ws, &hold)) != FA_OK)
         return rc;
     return fa::launch_decode_stall(q, k_pages, v_pages, page_table, seq_lens, o, B, H, d,
                                    page_size, ws, s->err, s->num_sms, st,
@@ -715,16 +720,14 @@ int fa_selftest_decode_stall(const void* q, const void* k_pages, const void* v_p
 }
 
 int fa_release_workspace(void) {
-    std::lock_guard<std::mutex> lock(g_mu);
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return FA_OK;
-    DeviceState& s = g_dev[dev];
-    if (!s.ws.empty()) {
+    const auto blocks = g_dev[dev].ws.clear();  // waits for calls that are being made
+    if (!blocks.empty()) {
         if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
-        for (StreamWorkspace& w : s.ws)
-            if (w.ptr && cudaFree(w.ptr) != cudaSuccess) return FA_ERR_CUDA;
-        s.ws.clear();
+        for (const auto& w : blocks)
+            if (w->ptr && cudaFree(w->ptr) != cudaSuccess) return FA_ERR_CUDA;
     }
     return FA_OK;
 }

@@ -1241,9 +1241,11 @@ int fa_decode_paged_fp8(const void* q, const void* k_pages, const void* v_pages,
         solo || fa::is_short(few, B, H_kv, d, max_pages, table_len) ? few : most;
     const size_t need = fa::scratch_bytes(B, H, H_kv, d, num_sms);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    fa::WorkspaceHold hold;
     if (!solo) {
         void* ws = nullptr;
-        if ((rc = fa::call_workspace(workspace, workspace_bytes, need, st, &ws)) != FA_OK) return rc;
+        if ((rc = fa::call_workspace(workspace, workspace_bytes, need, st, &ws, &hold)) != FA_OK)
+            return rc;
         p.seqs = static_cast<int64_t*>(ws);
         p.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + s.seqs_bytes);
         p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + s.seqs_bytes + s.lse_bytes);

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "fa.h"
+#include "workspace.h"
 
 // A bounded device wait gives up after this much global time.
 #define FA_WAIT_TIMEOUT_NS 2000000000ull
@@ -124,8 +125,10 @@ int device_error_word(unsigned int** err, int* num_sms);
 // than `need`), or with none given the library's workspace of the stream.  The
 // library's is refused (FA_ERR_UNSUPPORTED) while the stream is being captured:
 // an allocation would belong to the graph, and a second graph of the stream
-// would hold the same addresses.
-int call_workspace(void* workspace, int given, size_t need, cudaStream_t stream, void** out);
+// would hold the same addresses.  It is the call's until `hold` is destroyed: after
+// its last launch.
+int call_workspace(void* workspace, int given, size_t need, cudaStream_t stream, void** out,
+                   WorkspaceHold* hold);
 
 // ---- rotary tables, norms with the rotation --------------------------------
 constexpr int kRopeMaxPairs = 128;  // of a table's row

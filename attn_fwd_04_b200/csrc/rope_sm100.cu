@@ -577,10 +577,11 @@ int fa_qk_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const 
     const int ctas = fa::set_grid(p, static_cast<int64_t>(B) * N, d, fa::kBwdHeads, fa::kBwdCtas,
                                   num_sms);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    fa::WorkspaceHold hold;
     if (q_weight || k_weight) {
         void* ws = nullptr;
         const size_t need = sizeof(float) * static_cast<size_t>(ctas) * d;
-        if ((rc = fa::call_workspace(workspace, workspace_bytes, need, st, &ws)) != FA_OK)
+        if ((rc = fa::call_workspace(workspace, workspace_bytes, need, st, &ws, &hold)) != FA_OK)
             return rc;
         p.part = static_cast<float*>(ws);
     }

@@ -46,7 +46,10 @@
  *    They belong to the GPU's primary context: do not keep using the library
  *    across a cudaDeviceReset (which destroys that context).
  *  - Thread safety: the host entry points may be called from several host
- *    threads; the workspace bookkeeping is guarded by a mutex.
+ *    threads, on one stream too: a call that uses its stream's workspace holds
+ *    it from its lookup to its last launch, and another thread's call on that
+ *    stream waits as long.  A workspace given by the caller is the caller's to
+ *    keep from two calls at once.
  */
 #ifndef FA_H
 #define FA_H
