@@ -78,7 +78,9 @@ const void* optional(PyObject* o, ScalarType type, at::IntArrayRef sizes) {
 int token_stride(const Tensor& t) {
     need(t.scalar_type() == ScalarType::BFloat16 && t.dim() == 3);
     const int64_t row = t.size(1) * t.size(2), st = t.stride(0);
-    need(t.stride(2) == 1 && t.stride(1) == t.size(2) && st >= row && st % 8 == 0);
+    // (torch gives a dimension of one any stride)
+    need(t.stride(2) == 1 && (t.stride(1) == t.size(2) || t.size(1) == 1) && st >= row &&
+         st % 8 == 0);
     return fit(st);
 }
 

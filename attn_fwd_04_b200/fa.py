@@ -707,7 +707,8 @@ def _token_rows(t, name: str, dev=None, shape=None) -> int:
         raise ValueError(f"{name} is on {t.device}, the call's inputs on GPU {dev}")
     tokens, heads, d = mine
     st, sh, sd = t.stride()
-    if sd == 1 and sh == d and heads * d <= st < 1 << 31 and st % 8 == 0:
+    # (torch gives a dimension of one any stride)
+    if sd == 1 and (sh == d or heads == 1) and heads * d <= st < 1 << 31 and st % 8 == 0:
         return st
     if (sd != 1 and d > 1) or (sh != d and heads > 1):
         raise ValueError(f"{name}: the [heads, d] part of a token must be contiguous")
