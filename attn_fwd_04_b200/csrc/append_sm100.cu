@@ -762,7 +762,7 @@ __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block 
         if (live && lane.chunk == 0) *scale = now;
         for (int c = chunks - 1; c >= 0; --c) {
             if (c < chunks - 1) {
-                fetch(pair, c);
+                if (c == 0 && base == pair_begin) fetch(pair, c);  // (take has the others)
                 take(c);
             }
 #pragma unroll

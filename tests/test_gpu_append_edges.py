@@ -62,3 +62,58 @@ def test_a_sequence_of_2_31_tokens(eight, n, d, block):
         assert torch.equal(now[0], was[0])
         assert torch.equal(now[1, :, :255 - n], was[1, :, :255 - n])
         assert torch.equal(now[1, :, 255], was[1, :, 255])
+
+
+@pytest.mark.parametrize("d,block,heads", [(128, 256, 8), (64, 64, 20), (128, 16, 1)])
+def test_a_longer_prompt_among_single_tokens(d, block, heads):
+    """So few new tokens on average that every block takes the way of a decode step:
+    the one prompt's blocks go through it a few rows at a time, and back."""
+    new = [1] * 40 + [130] + [1] * 23
+    ctx = [(37 * i) % 300 for i in range(64)]
+    ctx[40] = 250
+    lens = [n + c for n, c in zip(new, ctx)]
+    g = torch.Generator().manual_seed(d + block)
+    total, P = sum(new), sum(ref.pages_of(lens))
+    k, v = ((torch.randn((total, heads, d), generator=g) *
+             torch.exp2(torch.randint(-3, 4, (total, heads, 1), generator=g))).bfloat16().cuda()
+            for _ in range(2))
+    cu = torch.tensor([0] + list(torch.tensor(new).cumsum(0))).int().cuda()
+    table = torch.randperm(P, generator=g).int()
+    w = (1 + 0.3 * torch.randn(d, generator=g)).cuda()
+    cos, sin = fa.fa_rope_table(1024, d)
+    shape = (P, heads, PS, d)
+    kp, vp = (torch.randn(shape, generator=g).to(FP8).cuda() for _ in range(2))
+    # small scales: every block that had tokens grows
+    ks, vs = (torch.full((P, heads, PS // block), 2.0 ** -12, device="cuda") for _ in range(2))
+    old = [t.float().double() for t in (kp, vp)]
+    fa.fa_append_paged_fp8(None, k, v, cu, kp, vp, ks, vs, table.cuda(),
+                           torch.tensor(lens).int().cuda(), cos, sin, None, w, eps=1e-5)
+    _ok()
+    at = 0
+    for b, (n, c) in enumerate(zip(new, ctx)):
+        pos = torch.arange(c, c + n, device="cuda")
+        turned = ref.norm_rope(k[at:at + n], w, cos[pos], sin[pos], False, 1e-5)
+        pages = ref.page_list(table, lens, b)
+        for pool, s, was, x, slack in ((kp, ks, old[0], turned, 2.0 ** -19),
+                                       (vp, vs, old[1], v[at:at + n].double(), 0.0)):
+            got = ref.gather(pool, s, pages, c + n)
+            for lo in range(c // block * block, c + n, block):
+                hi, first = min(lo + block, c + n), max(lo, c)
+                rows = x[first - c:hi - c]
+                scale = s[pages[lo // PS], :, lo % PS // block].double()
+                top = rows.abs().amax((0, 2))
+                # the least power of two that the block's values need (or one that the
+                # fp32 values' own rounding needs)
+                least = torch.tensor([ref.least_scale(t) for t in top.tolist()]).cuda().double()
+                near = torch.tensor([ref.least_scale(t) for t in (top * (1 + 2 * slack)).tolist()]
+                                    ).cuda().double()
+                assert ((scale == least) | (scale == near)).all()
+                # half a step of 4 bits or of the least codes, and the values' fp32 rounding
+                tol = 2.0 ** -4 * rows.abs() + 2.0 ** -10 * scale[:, None] + \
+                    slack * rows.abs().amax(-1, keepdim=True)
+                assert ((got[first:hi] - rows).abs() <= tol).all()
+                kept = was[pages[lo // PS], :, lo % PS:lo % PS + first - lo].transpose(0, 1) * \
+                    2.0 ** -12
+                tol = 2.0 ** -4 * kept.abs() + 2.0 ** -10 * scale[:, None]
+                assert ((got[lo:first] - kept).abs() <= tol).all()
+        at += n
