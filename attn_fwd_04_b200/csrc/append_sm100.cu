@@ -142,7 +142,7 @@ __device__ __forceinline__ void place_rows(const Append& p, int first, int count
             bool bad;
             len = __ldg(p.lens + i);
             rows_of(p, i, r0, n, bad);
-            if (bad) record_error(p.err, FA_DEVERR_BAD_INPUT);
+            if (bad || n > len) record_error(p.err, FA_DEVERR_BAD_INPUT);
         }
         const int lo = max(r0, first), hi = min(r0 + n, first + count);
         for (int r = lo; r < hi; ++r) atomicMax(&sh.seq[r - first], i);  // overlapping: the last
@@ -337,12 +337,15 @@ __device__ __forceinline__ void decode8(const uint2& u, float (&y)[8]) {
 }
 
 // The new tokens of (sequence, block) number `unit`: the blocks that hold new
-// rows are counted over the sequences.
+// rows are counted over the sequences.  One CTA of a launch without queries (whose
+// rows' CTAs look at all sequences) looks at those behind its unit too, so that what
+// is wrong with them is reported.
 __device__ __forceinline__ bool find_unit(const Append& p, int unit, Shared& sh, Seq& s,
                                           int& blk) {
     const int lg = p.block_log2;
     int64_t before = 0, pages = 0;  // of the sequences scanned
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool all = blockIdx.x == 0 && !p.q;
     if (threadIdx.x == 0) sh.blk = -1;
     for (int base = 0; base < p.B; base += kThreads) {
         const int i = base + threadIdx.x;
@@ -391,7 +394,7 @@ __device__ __forceinline__ bool find_unit(const Append& p, int unit, Shared& sh,
         before += all_units;
         pages += all_pages;
         __syncthreads();
-        if (before > unit) break;
+        if (before > unit && !all) break;
     }
     blk = sh.blk;
     if (blk < 0) return false;

@@ -551,10 +551,10 @@ FA_API int fa_qk_norm_rope_bwd_workspace(int B, int N, int H, int H_kv, int d, i
  *   q_weight, k_weight, weight_type, rope_cos, rope_sin, max_pos, rotary_dim,
  *   interleaved, eps : as fa_qk_norm_rope; a token's position is its place in
  *            the cache, seq_lens[b] - n_b + i
- * A sequence with more new rows than tokens, longer than max_pos (with a
- * rotation), or with more pages than its table holds is reported as
- * FA_ERR_DEVICE_BAD_INPUT: its q_out rows are zeros and nothing of it is
- * stored.  Offsets outside [0, total_new] and page indices outside
+ * A sequence with more new rows than tokens (a negative length among them), or
+ * with new rows and longer than max_pos (with a rotation) or with more pages than
+ * its table holds, is reported as FA_ERR_DEVICE_BAD_INPUT: its q_out rows are zeros
+ * and nothing of it is stored.  Offsets outside [0, total_new] and page indices outside
  * [0, num_pages) are reported and skipped.  Rows that no sequence holds are
  * left as they were, in q_out too.  Pages being written must belong to one
  * sequence each (a shared page's new rows would be written twice, in either

@@ -117,3 +117,38 @@ def test_a_longer_prompt_among_single_tokens(d, block, heads):
                 tol = 2.0 ** -4 * kept.abs() + 2.0 ** -10 * scale[:, None]
                 assert ((got[lo:first] - kept).abs() <= tol).all()
         at += n
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("with_q", [False, True])
+@pytest.mark.parametrize("fault", ["offset", "length"])
+def test_a_fault_behind_the_last_new_row_is_reported(eight, with_q, fault):
+    """300 sequences, the first 256 with the new rows; something is wrong with one of
+    the others, which none of those rows belongs to."""
+    B, Hk, d = 300, 2, 64
+    g = torch.Generator().manual_seed(0)
+    q, k, v = (torch.randn((256, h, d), generator=g).bfloat16().cuda() for h in (4, Hk, Hk))
+    cu = torch.arange(B + 1).clamp(max=256).int()
+    lens = torch.ones(B, dtype=torch.int32)
+    lens[256:] = 0
+    table = torch.arange(256).int().cuda()
+    outs = []
+    for bad in (False, True):
+        c, n = cu.clone(), lens.clone()
+        if bad and fault == "offset":
+            c[290] = 257
+        if bad and fault == "length":
+            n[290] = -3
+        dt = FP8 if eight else torch.bfloat16
+        kp, vp = (torch.zeros((256, Hk, PS, d), device="cuda").to(dt) for _ in range(2))
+        ks, vs = (torch.ones((256, Hk, 4), device="cuda") for _ in range(2))
+        a = [q if with_q else None, k, v, c.cuda(), kp, vp, table, n.cuda()]
+        if eight:
+            a[6:6] = [ks, vs]
+        f = fa.fa_append_paged_fp8 if eight else fa.fa_append_paged_rope
+        out = f(*a)
+        want = fa.FA_ERR_DEVICE_BAD_INPUT if bad else fa.FA_OK
+        assert fa.fa_get_device_error() == want
+        outs.append([kp.view(torch.uint8), vp.view(torch.uint8), ks, vs] + [out] * with_q)
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)
