@@ -493,6 +493,7 @@ int fa_rope_table(float* rope_cos, float* rope_sin, int max_pos, int rotary_dim,
             slow = std::fmin(1.0, std::fmax(0.0, (i - first) / std::fmax(last - first, 0.001)));
         if (slow > 0.0) w = w * (1.0 - slow) + w / factor * slow;
         t.w[i] = w / fa::kTwoPi;
+        if (!std::isfinite(t.w[i] * max_pos)) return FA_ERR_SHAPE;  // no angle
     }
     unsigned int* err = nullptr;
     int num_sms = 0, rc;

@@ -457,8 +457,9 @@ enum fa_layout {
  * The arguments that a scaling does not name are not looked at.  Angles are
  * formed and reduced in fp64, so far positions keep their accuracy.
  * Errors: FA_ERR_SHAPE for max_pos < 1, an odd or out-of-range rotary_dim,
- * base <= 1, factor <= 0, high <= low, original_len < 1, or a value that is
- * not finite; FA_ERR_UNSUPPORTED for another scaling.
+ * base <= 1, factor <= 0, high <= low, original_len < 1, a value that is
+ * not finite, or angles that fp64 does not hold; FA_ERR_UNSUPPORTED for another
+ * scaling.
  */
 FA_API int fa_rope_table(float* rope_cos, float* rope_sin, int max_pos, int rotary_dim,
                          double base, int scaling, double factor, int original_len, double low,
