@@ -18,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libfa.so")
 CALLS = os.path.join(PKG, "_calls.so")
+CALLS_TORCH = os.path.join(PKG, "_build", "calls.torch")  # what it was built against
 SOURCES = ["api.cu", "fwd_sm100.cu", "bwd_sm100.cu", "decode_sm100.cu", "decode_noalloc.cu",
            "rope_sm100.cu", "append_sm100.cu", "decode_fp8_sm100.cu"]
 HEADERS = ["fa_ptx.cuh", "fa_internal.h", "rope_row.cuh", "workspace.h"]
@@ -44,12 +45,22 @@ def _stale(out: str, deps) -> bool:
     return any(os.path.getmtime(p) > t for p in deps)
 
 
+def _torch_of_calls() -> str:
+    """The torch that CALLS was built against; empty: unknown."""
+    try:
+        with open(CALLS_TORCH) as f:
+            return f.read().strip()
+    except OSError:
+        return ""
+
+
 def _build_calls(force: bool, verbose: bool) -> None:
     """_calls.so, against the headers and libraries of the torch that runs this."""
     src = os.path.join(CSRC, "calls.cpp")
-    if not force and not _stale(CALLS, [src]):
-        return
     import torch
+    built_for = f"{torch.__version__} python {sys.version.split()[0]}"
+    if not force and not _stale(CALLS, [src]) and _torch_of_calls() == built_for:
+        return
     root = os.path.dirname(torch.__file__)
     headers = [os.path.join(root, "include"),
                os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -64,6 +75,9 @@ def _build_calls(force: bool, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    os.makedirs(os.path.dirname(CALLS_TORCH), exist_ok=True)
+    with open(CALLS_TORCH, "w") as f:
+        f.write(built_for + "\n")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

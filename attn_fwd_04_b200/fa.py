@@ -606,12 +606,19 @@ def _short():
         L = lib()
         try:
             from . import _calls
-        except ImportError as e:
+            _same_torch(_calls.torch_version)
+        except (ImportError, AttributeError) as e:
             raise ImportError("the binding's _calls.so is missing or of another torch; build "
                               "it with `python -m attn_fwd_04_b200.build`") from e
         _calls.bind(tuple(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _SHORT))
         _short_calls = _calls
     return _short_calls
+
+
+def _same_torch(built_for: str):
+    """Tensors are read through torch's own C++ classes: one version's only."""
+    if not torch.__version__.startswith(built_for):
+        raise ImportError(f"built for torch {built_for}, this is {torch.__version__}")
 
 
 def _answer(out, name: str):
