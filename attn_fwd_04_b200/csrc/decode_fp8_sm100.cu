@@ -28,8 +28,8 @@
 // memory to registers in whole 128-byte rows, 8 KB a warp in flight, and only
 // V's bytes are paired across two tokens (a byte permute).  S^T's accumulators
 // are P^T's operand after one 8 x 8 transpose in registers.  8 query heads
-// fill an instruction's 8 columns; up to 16 take two of them, more are split
-// into groups, a warp each, over the same tokens.
+// fill an instruction's 8 columns; up to 24 take two or three of them, more are
+// split into groups, a warp each, over the same tokens.
 // (With the heads in the 16 rows instead, 8 heads would leave half of every
 // instruction and half of the accumulators empty.)
 //
@@ -349,12 +349,11 @@ __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
 // room for a tile on its way, so each warp has a ring of two tiles of its own,
 // filled by asynchronous copies of 16 bytes one tile ahead.  Where the pieces go is
 // permuted within 128-byte lines so that the 8 lanes of a phase of a fragment's load
-// find 8 different ones.  Up to 32 heads share a warp, and so one conversion of the
+// find 8 different ones.  Up to 24 heads share a warp, and so one conversion of the
 // tile's bytes.
 //
-// 64 sequences of 8K to 16K tokens, 4 K/V heads of 16 query heads: 154 us, 0.84 of a
-// copy (tiles in registers 178); of 24 197 and of 32 258 (as groups of 12 and of 16,
-// side by side on the same bytes, 264 and 266): the products bound them, some 64 us
+// 64 sequences of 8K to 16K tokens, 4 K/V heads of 16 query heads: 169 us, 0.74 of a
+// copy; of 24 229, of 32 (two groups of 16) 326: the products bound them, some 75 us
 // for every 8 heads.
 constexpr int kStages = 2;  // (three leave room for one CTA an SM only)
 constexpr int stage_bytes(int d) { return 2 * tile_tokens(d) * d + 128; }  // K, V, scales
@@ -1077,7 +1076,10 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 // How the query heads of a K/V head and the warps are cut: up to kMostHeads of them
 // to a warp, kFewHeads where the stream is short or a sequence's head has CTAs of its
 // own, and more warps are worth more than fewer products and conversions.
-constexpr int kMostHeads = 32, kFewHeads = 16;
+// (64 sequences of 8K to 16K tokens, 24 heads for each of 4 K/V heads 229 us in one
+// group, 324 in two; 32 heads in one group of 32, whose registers spill, 310 and 102 for
+// one K/V head, in two of 16 326 and 96.)
+constexpr int kMostHeads = 24, kFewHeads = 16;
 struct Shape {
     int groups, group_heads, nt, ctas, ranges;
     size_t seqs_bytes, lse_bytes, bytes;  // of the workspace: sequences, sums, pieces
@@ -1108,7 +1110,8 @@ size_t scratch_bytes(int B, int H, int H_kv, int d, int num_sms) {
 }
 
 // Up to four tiles a warp, as far as the table tells (one sequence of 32K tokens with
-// one K/V head of 32: 16 us in groups of 16 heads, 25 in one of 32).
+// one K/V head of 48: 18 us in groups of 16 heads, 25 in groups of 24; 64 sequences of 2K
+// to 4K tokens, seven tiles a warp, with one of 24 36 and 33).
 bool is_short(const Shape& s, int B, int H_kv, int d, int max_pages, int table_len) {
     const int64_t entries = max_pages ? static_cast<int64_t>(B) * max_pages : table_len;
     return entries * (kPage / tile_tokens(d)) * H_kv <= 4 * static_cast<int64_t>(s.ranges);
@@ -1152,8 +1155,7 @@ template <int D>
 int launch(const DecodeFp8& p, const Shape& s, cudaStream_t st) {
     auto split = s.nt == 1   ? fa_decode_fp8_split_kernel<D, 1, 0, false>
                  : s.nt == 2 ? fa_decode_fp8_split_kernel<D, 2, 0, true>
-                 : s.nt == 3 ? fa_decode_fp8_split_kernel<D, 3, 0, true>
-                             : fa_decode_fp8_split_kernel<D, 4, 0, true>;
+                             : fa_decode_fp8_split_kernel<D, 3, 0, true>;
     const int ring = s.nt > 1 ? ring_bytes(D) : 0;
     if (ring && cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, ring) !=
                     cudaSuccess)
