@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 // meanwhile.  The positions' rotations are read from L1 again for each head (kept in
 // registers, 32 of them, blocks of 128 took 105 us instead of 93).
 //
-// 8 x 1024 tokens of 32 + 2 * 32 heads, blocks of 64: 79 us, 4.3 TB/s, 0.66 of a
-// copy; of it the queries 23 us (at their floor) and keys and values some 56 (31).
+// 8 x 1024 tokens of 32 + 2 * 32 heads, blocks of 64: 76 us, 4.5 TB/s, 0.69 of a
+// copy; of it the queries 23 us (at their floor) and keys and values some 54 (31).
 // Those are bound by latency: a barrier a head, two CTAs of 128 registers an SM
 // (three spill: 109 us without the queries), the scheduler 46 % busy.  With the
 // rows read twice instead of kept, 132 us; with them fetched into registers one
@@ -691,7 +691,10 @@ __device__ __forceinline__ void append_block(const Append& p, const Block& b, bo
 // slot takes one head of K or of V (pairs pair_begin .. pair_end - 1, the keys
 // first), R tokens at a time, and finds its scale alone; where scales grow,
 // the CTA rounds the earlier tokens of those heads together.  A step of 64 tokens
-// with 32 + 2 * 8 heads takes 4.5 us, as into bf16 pages.
+// with 32 + 2 * 8 heads takes 4.5 to 5.1 us, into bf16 pages 4.5.  (A longer prompt
+// among so many single tokens that their mean is small goes R rows at a time through
+// one CTA for each of its blocks and heads: 190 tokens beside 63 single ones 60 us in
+// blocks of 64, 150 in blocks of 256.)
 template <int D, bool INTER, int R>
 __device__ __forceinline__ void append_few(const Append& p, const Seq& s, Block b, int pair_begin,
                                            int pair_end) {
@@ -952,7 +955,7 @@ template <int D, bool INTER>
 int launch_fp8(Append& p, int num_sms, cudaStream_t st) {
     // Sequences with a few tokens each: a slot takes a head, and a unit's heads go
     // to as many CTAs as make two an SM, the rows' CTAs among them (a step of 64
-    // tokens 6.3 us, with one CTA too many an SM 8.1).  Else up to 16 heads of a
+    // tokens 4.5 us, with one CTA more an SM 6.2).  Else up to 16 heads of a
     // unit one after the other, and fewer where SMs would be short of CTAs.
     const int row_ctas = p.q ? (p.total + p.tokens - 1) / p.tokens : 0;
     const bool few = p.total <= static_cast<int64_t>(p.B) * kRows;

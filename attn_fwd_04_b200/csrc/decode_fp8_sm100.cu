@@ -33,13 +33,12 @@
 // (With the heads in the 16 rows instead, 8 heads would leave half of every
 // instruction and half of the accumulators empty.)
 //
-// 64 sequences of 1K to 32K tokens, 8 K/V heads and 32 query heads: 341 us, 6.6
-// TB/s, 1.02 of a copy, every byte read once; with 32 K/V heads and up to 16K tokens
-// 689 us, 6.7 TB/s.  Run on end for seconds the board's 1000 W bound it instead: 383
-// and 775 us at 1.6 GHz, hardly less with the products left out (384) or the
-// conversions (387).  The scheduler is 40 % busy, the tensor pipe 20 %.  A stream of
-// few tiles is bound by latency: 12 us for 8 x 2048 tokens, of which a copy would
-// take 4.
+// 64 sequences of 1K to 32K tokens, 8 K/V heads and 32 query heads: 354 us, 6.4
+// TB/s, 0.98 of a copy, every byte read once; with 32 K/V heads and up to 16K tokens
+// 718 us, 6.5 TB/s.  Run on end for seconds the board's 1000 W bound it instead: 385
+// and 776 us at 1.6 GHz.  The scheduler is 40 % busy, the tensor pipe 28 %.  A stream of
+// few tiles is bound by latency: 14 us for 8 x 2048 tokens, of which a copy would
+// take 5.
 //
 // Rounding: each query row is scaled by a power of two into fp16, which holds
 // its 8 bits exactly down to 2^-31 of the row's largest; scores, maxima and sums
@@ -49,7 +48,8 @@
 // push the others out of fp16's range, whatever the scales.  A weight is the sum of
 // two fp16 values (22 bits, or 2^-40 of the largest), each with a product of its own:
 // with one alone an output differed by 1e-3 of its size from that of fp32 weights, now
-// by 2e-4 and less, which is what bf16 makes of fp32 sums in another order.
+// by 2e-4, which is what bf16 makes of fp32 sums in another order.  It costs 2 % of the
+// time above, and 14 to 36 % where more than 8 query heads share a K/V head (below).
 #include <algorithm>
 #include <cmath>
 
@@ -354,7 +354,8 @@ __device__ __forceinline__ void advance(const DecodeFp8& p, Cursor& c) {
 //
 // 64 sequences of 8K to 16K tokens, 4 K/V heads of 16 query heads: 169 us, 0.74 of a
 // copy; of 24 229, of 32 (two groups of 16) 326: the products bound them, some 75 us
-// for every 8 heads.
+// for every 8 heads.  (With one product for the weights 148, 188, and 240 for 32 in one
+// group.)
 constexpr int kStages = 2;  // (three leave room for one CTA an SM only)
 constexpr int stage_bytes(int d) { return 2 * tile_tokens(d) * d + 128; }  // K, V, scales
 constexpr int ring_bytes(int d) { return kWarps * kStages * stage_bytes(d); }

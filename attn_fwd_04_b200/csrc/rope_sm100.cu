@@ -20,8 +20,8 @@ constexpr int kThreads = 256;
 constexpr int kFwdHeads = 4;  // heads a slot takes
 constexpr int kBwdHeads = 4;
 constexpr int kFwdCtas = 32;  // CTAs per SM of the grids, at most
-// The backward grid is what is resident: 3 CTAs of 80 registers an SM, 220 us
-// for 36800 tokens of 40 heads; 2 heads a slot 238, 6 CTAs in two waves 243.
+// The backward grid is what is resident: 3 CTAs of 80 registers an SM (figures at the
+// kernel).
 constexpr int kBwdCtas = 3;
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
@@ -215,8 +215,8 @@ __global__ void __launch_bounds__(kThreads, 4)
 // x is read again and normed again: cheaper than a saved statistic.  Each
 // thread sums dw over its rows in registers, the CTA over its threads in
 // shared memory, and a second kernel over the CTAs in fp64: a fixed order.
-// 36800 packed tokens of 32 + 8 heads: 196 us with the second kernel, 5.8 TB/s,
-// 0.90 of a copy; memory latency leads the stalls, with the scheduler over half
+// 36800 packed tokens of 32 + 8 heads: 196 to 203 us with the second kernel (of
+// several machines), 5.6 to 5.8 TB/s, up to 0.90 of a copy; memory latency leads the stalls, with the scheduler over half
 // busy (3 heads a slot 208 us, 2 heads and 4 CTAs an SM 210, 6 and 2 242).
 template <int D, bool INTER, bool HEADS, int U>
 __global__ void __launch_bounds__(kThreads, kBwdCtas)

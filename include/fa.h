@@ -589,6 +589,11 @@ FA_API int fa_append_paged_rope(const void* q_new, const void* k_new, const void
  * 448 * 2^64 are stored as NaN.  Present scales must be within [2^-64, 2^64].
  * Everything else as fa_append_paged_rope; a block whose page index is out of
  * range is skipped.  block outside the list: FA_ERR_UNSUPPORTED.
+ * What reads these pages is fa_decode_paged_fp8, one query a sequence.
+ * fa_prefill_paged and fa_gather_paged take bf16 pages: a prompt without cached
+ * tokens before it attends by fa_qk_norm_rope and fa_fwd_varlen_gqa beside this
+ * call (without a rotation here, of the turned keys); one behind 8-bit pages has
+ * no call.
  */
 FA_API int fa_append_paged_fp8(const void* q_new, const void* k_new, const void* v_new,
                                const int32_t* cu_new, void* q_out, void* k_pages, void* v_pages,
