@@ -723,13 +723,18 @@ int fa_release_workspace(void) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
     if (dev < 0 || dev >= kMaxDevices) return FA_OK;
-    const auto blocks = g_dev[dev].ws.clear();  // waits for calls that are being made
-    if (!blocks.empty()) {
-        if (cudaDeviceSynchronize() != cudaSuccess) return FA_ERR_CUDA;
-        for (const auto& w : blocks)
-            if (w->ptr && cudaFree(w->ptr) != cudaSuccess) return FA_ERR_CUDA;
+    try {
+        const auto blocks = g_dev[dev].ws.clear();  // waits for calls that are being made
+        if (blocks.empty()) return FA_OK;
+        bool ok = cudaDeviceSynchronize() == cudaSuccess;
+        for (const auto& w : blocks) {
+            if (ok && w->ptr) ok = cudaFree(w->ptr) == cudaSuccess;
+            if (!ok) g_dev[dev].ws.keep(w);
+        }
+        return ok ? FA_OK : FA_ERR_CUDA;
+    } catch (...) {
+        return FA_ERR_NOMEM;
     }
-    return FA_OK;
 }
 
 const char* fa_status_str(int status) {

@@ -45,15 +45,23 @@ class StreamBlocks {
         }
     }
 
-    // All blocks, none of them held, no longer anyone's.
+    // All blocks, none of them held, no longer anyone's: for the caller to free.
     std::vector<std::shared_ptr<StreamBlock>> clear() {
         std::vector<std::shared_ptr<StreamBlock>> out;
         {
             std::lock_guard<std::mutex> lock(mu_);
+            all_.insert(all_.end(), unfreed_.begin(), unfreed_.end());
+            unfreed_.clear();
             out.swap(all_);
         }
         for (auto& b : out) WorkspaceHold(b)->gone = true;
         return out;
+    }
+
+    // One of those that could not be freed: the next clear gives it again.
+    void keep(std::shared_ptr<StreamBlock> b) {
+        std::lock_guard<std::mutex> lock(mu_);
+        unfreed_.push_back(std::move(b));
     }
 
   private:
@@ -68,7 +76,7 @@ class StreamBlocks {
     }
 
     std::mutex mu_;
-    std::vector<std::shared_ptr<StreamBlock>> all_;
+    std::vector<std::shared_ptr<StreamBlock>> all_, unfreed_;
 };
 
 }  // namespace fa

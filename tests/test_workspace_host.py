@@ -81,6 +81,13 @@ int main() {
     release.join();
     if (!old || !old->gone) return std::printf("not released\n"), 4;
     if (blocks.take(&a)->bytes != 0) return std::printf("released block used\n"), 5;
+    // what could not be freed comes again, and is nobody's meanwhile
+    blocks.clear();
+    blocks.keep(old);
+    if (blocks.take(&a)->bytes != 0) return std::printf("kept block used\n"), 6;
+    int again = 0;
+    for (auto& x : blocks.clear()) again += x == old;
+    if (again != 1 || !blocks.clear().empty()) return std::printf("kept block lost\n"), 7;
     std::printf("ok\n");
     return 0;
 }
